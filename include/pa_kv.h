@@ -112,6 +112,95 @@ pa_status pa_kv_cache_write(const pa_kv_cache* cache, const void* k, const void*
                             const int64_t* slot_mapping, int32_t* dev_status, pa_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Norms of the queries and keys of each head, the rotary position rotation and
+ * the cache write.  (The pages start from ready queries and keys; a decoder
+ * layer gets them this way: the new token's K/V of "Как работает paged
+ * attention?" 4.1 are its normed and rotated projections.)
+ *
+ * Frequencies.  Pair i < rotary_dim/2 of a head's rotated part turns by
+ * position * theta_i radians, theta_i = base^(-2i/rotary_dim), changed for
+ * longer contexts by `scaling` (NULL: not at all):
+ *   PA_ROPE_LINEAR  theta_i / factor
+ *   PA_ROPE_NTK     theta_i of the base  base * factor^(r/(r-2)), r = rotary_dim
+ *   PA_ROPE_YARN    theta_i (1 - g) + theta_i / factor * g, g going linearly from 0
+ *                   at pair  floor(at(beta_fast))  to 1 at  ceil(at(beta_slow)),
+ *                   at(x) = r ln(original_max_position / (2 pi x)) / (2 ln base)
+ *                   (both clipped to 0 .. r-1); cos and sin times 0.1 ln(factor) + 1
+ *   PA_ROPE_BANDED  theta_i w + theta_i / factor * (1 - w), with the pair's turns over
+ *                   the original context  c = original_max_position theta_i / (2 pi):
+ *                   w = clip((c - low_freq_factor) / (high_freq_factor -
+ *                   low_freq_factor), 0, 1)
+ *   PA_ROPE_GIVEN   inv_freq holds the caller's own theta_i (an input; any finite values)
+ * pa_rope_frequencies is a host call on host arrays: it writes inv_freq
+ * [rotary_dim/2] (theta_i) and turns [rotary_dim/2], the same as turns per position
+ * in units of 2^-64 (what the kernels read: copy it to the device once), and the
+ * factor of cos and sin.  rotary_dim even and >= 2, base > 1, factor >= 1.
+ * ------------------------------------------------------------------------- */
+typedef enum {
+    PA_ROPE_NONE = 0,
+    PA_ROPE_LINEAR = 1,
+    PA_ROPE_NTK = 2,
+    PA_ROPE_YARN = 3,
+    PA_ROPE_BANDED = 4,
+    PA_ROPE_GIVEN = 5
+} pa_rope_kind;
+
+typedef struct {
+    pa_rope_kind kind;
+    double factor;
+    double original_max_position;             /* YARN, BANDED */
+    double beta_fast, beta_slow;              /* YARN */
+    double low_freq_factor, high_freq_factor; /* BANDED */
+} pa_rope_scaling;
+
+pa_status pa_rope_frequencies(int32_t rotary_dim, double base, const pa_rope_scaling* scaling, double* inv_freq,
+                              uint64_t* turns, float* rope_factor);
+
+/* What is done to a head's row x of D = head_size elements (host struct, device
+ * pointers):
+ *     y = x / sqrt(mean(x^2) + eps) * weight    (weight NULL: y = x)
+ *     out_a = rope_factor (y_a cos(p theta_i) - y_b sin(p theta_i))
+ *     out_b = rope_factor (y_b cos(p theta_i) + y_a sin(p theta_i))
+ * for the pairs i < rotary_dim/2 of the first rotary_dim elements, (a, b) = (i, i +
+ * rotary_dim/2), or (2i, 2i + 1) when interleaved != 0; the other elements are y.
+ * p is the token's position.  Everything is computed in binary32 and rounded
+ * once (to nearest even) to the output's type. */
+typedef struct {
+    const float* q_weight;   /* device [head_size], 16-byte aligned; NULL: queries are not normed */
+    const float* k_weight;   /* likewise for the keys */
+    float eps;               /* > 0 where a weight is given */
+    const uint64_t* turns;   /* device [rotary_dim/2], from pa_rope_frequencies */
+    float rope_factor;
+    int32_t rotary_dim;      /* 0 (no rotation) or a multiple of 16, at most head_size */
+    int32_t interleaved;
+} pa_qk_transform;
+
+/* Queries and keys to packed rows (as pa_prefill_varlen_packed reads them).
+ * q, k: device rows of `dtype` (F16 or BF16), [num_tokens][num_heads or
+ *   num_kv_heads][head_size], consecutive tokens q_stride / k_stride elements apart
+ *   (views into a fused qkv buffer); q_out, k_out likewise.  Any alignment that the
+ *   type has (16-byte aligned pointers and strides go faster).  q_out may be q
+ *   itself with the same stride, and k_out k; no other overlap.
+ * positions: device int64 [num_tokens], any values (NULL when rotary_dim is 0).
+ * Supported: head_size 64 or 128; up to 4096 heads of each. */
+pa_status pa_qk_norm_rope(void* q_out, void* k_out, const void* q, const void* k, pa_dtype dtype, int64_t num_tokens,
+                          int32_t num_heads, int32_t num_kv_heads, int32_t head_size, int64_t q_stride,
+                          int64_t k_stride, int64_t q_out_stride, int64_t k_out_stride, const int64_t* positions,
+                          const pa_qk_transform* transform, pa_stream_t stream);
+
+/* The same with the keys and values written to their cache slots: queries to q_out,
+ * keys (normed and rotated) and values (as they are) to slot_mapping's slots, which
+ * work as in pa_kv_cache_write (s < 0: the token's K/V are not written, its queries
+ * still are; a slot past the cache is reported as PA_ERR_BAD_BLOCK).  A 16-bit cache
+ * has kv_dtype == dtype; an E4M3 cache stores e4m3_satfinite(round-to-nearest-even(
+ * out / scale)) of the binary32 out: no 16-bit rounding in between. */
+pa_status pa_qk_norm_rope_write(void* q_out, const void* q, const void* k, const void* v, pa_dtype dtype,
+                                const pa_kv_cache* cache, int64_t num_tokens, int32_t num_heads, int64_t q_stride,
+                                int64_t k_stride, int64_t v_stride, int64_t q_out_stride, const int64_t* positions,
+                                const int64_t* slot_mapping, const pa_qk_transform* transform, int32_t* dev_status,
+                                pa_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Copy whole physical blocks (all KV heads, K and V): the device half of
  * copy-on-write ("Как работает paged attention?" 3.3: a shared block is
  * copied before a sequence writes into it).

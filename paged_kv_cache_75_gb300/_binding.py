@@ -25,6 +25,17 @@ class _Cache(C.Structure):
                 ("kv_dtype", C.c_int), ("k_scale", C.c_float), ("v_scale", C.c_float)]
 
 
+class _RopeScaling(C.Structure):
+    _fields_ = [("kind", C.c_int), ("factor", C.c_double), ("original_max_position", C.c_double),
+                ("beta_fast", C.c_double), ("beta_slow", C.c_double), ("low_freq_factor", C.c_double),
+                ("high_freq_factor", C.c_double)]
+
+
+class _QKTransform(C.Structure):
+    _fields_ = [("q_weight", C.c_void_p), ("k_weight", C.c_void_p), ("eps", C.c_float), ("turns", C.c_void_p),
+                ("rope_factor", C.c_float), ("rotary_dim", C.c_int32), ("interleaved", C.c_int32)]
+
+
 def library():
     """The loaded C library; raises if it has not been built."""
     global _lib
@@ -39,6 +50,11 @@ def library():
             "pa_status_str": ([C.c_int], C.c_char_p),
             "pa_version": ([], i32),
             "pa_kv_cache_write": ([pc, vp, vp, C.c_int, i64, i64, vp, vp, vp], C.c_int),
+            "pa_rope_frequencies": ([i32, C.c_double, C.POINTER(_RopeScaling), vp, vp, C.POINTER(f32)], C.c_int),
+            "pa_qk_norm_rope": ([vp, vp, vp, vp, C.c_int, i64, i32, i32, i32, i64, i64, i64, i64, vp,
+                                 C.POINTER(_QKTransform), vp], C.c_int),
+            "pa_qk_norm_rope_write": ([vp, vp, vp, vp, C.c_int, pc, i64, i32, i64, i64, i64, i64, vp, vp,
+                                       C.POINTER(_QKTransform), vp, vp], C.c_int),
             "pa_copy_blocks": ([pc, vp, i32, vp, vp], C.c_int),
             "pa_decode_workspace_size": ([i32, i32, i32, i32, i32, i32], sz),
             "pa_decode": ([vp, vp, C.c_int, pc, vp, i32, vp, i32, i32, i32, f32, i32, vp, sz, vp, vp],
@@ -106,6 +122,23 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _stream(t: torch.Tensor):
     return C.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+
+
+class _Here:
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *a):
+        pass
+
+
+_here = _Here()
+
+
+def _on(device):
+    """The device of the call's tensors, as a context (nothing to do when it is
+    the current one already)."""
+    return _here if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
 def _need(t, name, dtype=None, cuda=True):
@@ -177,6 +210,151 @@ def pa_kv_cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slot_map
     st = library().pa_kv_cache_write(C.byref(cs), _ptr(k), _ptr(v), torch_dtype_code(k.dtype), T,
                                      k.stride(0), _ptr(slot_mapping), _ptr(dev_status), _stream(k))
     _check(st, "pa_kv_cache_write")
+
+
+ROPE_KINDS = ("none", "linear", "ntk", "yarn", "banded", "given")
+
+
+@dataclass
+class RopeFrequencies:
+    """Frequencies of a rotation: theta (radians per position, host float64
+    [rotary_dim/2]), turns (the same as turns per position in units of 2^-64,
+    int64 bits on the device that the kernels read), the factor of cos and sin."""
+    theta: "object"
+    turns: torch.Tensor
+    factor: float
+
+    @property
+    def rotary_dim(self):
+        return 2 * self.turns.shape[0]
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none", device="cuda",
+                     factor: float = 1.0, original_max_position: float = 0.0, beta_fast: float = 32.0,
+                     beta_slow: float = 1.0, low_freq_factor: float = 1.0, high_freq_factor: float = 4.0,
+                     theta=None) -> RopeFrequencies:
+    """Frequencies of a rotation over rotary_dim elements, scaled for long
+    contexts ("linear", "ntk", "yarn", "banded"; pa_rope_frequencies in
+    include/pa_kv.h has the formulas); "given" takes theta, radians per
+    position of each pair, as it is."""
+    import numpy as np
+    if scaling not in ROPE_KINDS:
+        raise ValueError("scaling must be one of %s" % (ROPE_KINDS,))
+    if (theta is not None) != (scaling == "given"):
+        raise ValueError("theta goes with scaling 'given'")
+    n = max(int(rotary_dim) // 2, 1)
+    th = np.zeros(n, np.float64)
+    if theta is not None:
+        th = np.array(theta, np.float64)  # a copy
+        if th.shape != (n,):
+            raise ValueError("theta must have rotary_dim / 2 entries")
+    turns = np.zeros(n, np.uint64)
+    out_factor = C.c_float(1.0)
+    sc = _RopeScaling(ROPE_KINDS.index(scaling), float(factor), float(original_max_position), float(beta_fast),
+                      float(beta_slow), float(low_freq_factor), float(high_freq_factor))
+    st = library().pa_rope_frequencies(int(rotary_dim), float(base), C.byref(sc), th.ctypes.data_as(C.c_void_p),
+                                       turns.ctypes.data_as(C.c_void_p), C.byref(out_factor))
+    _check(st, "pa_rope_frequencies")
+    return RopeFrequencies(th, torch.from_numpy(turns.view(np.int64)).to(device), float(out_factor.value))
+
+
+@dataclass
+class QKTransform:
+    """What pa_qk_norm_rope does to each head's row: the norm (q_weight,
+    k_weight: float32 [head_size]; None: not normed), then the rotation (rope;
+    None: none), in pairs (i, i + rotary_dim/2) or, interleaved, (2i, 2i+1)."""
+    rope: Optional[RopeFrequencies] = None
+    interleaved: bool = False
+    q_weight: Optional[torch.Tensor] = None
+    k_weight: Optional[torch.Tensor] = None
+    eps: float = 1e-6
+
+    def __post_init__(self):
+        for name, w in (("q_weight", self.q_weight), ("k_weight", self.k_weight)):
+            if w is not None:
+                _need(w, name, torch.float32)
+        if self.rope is not None:
+            _need(self.rope.turns, "rope.turns", torch.int64)
+
+    def c_struct(self, head_size: int, device) -> _QKTransform:
+        r = self.rope
+        for name, w in (("q_weight", self.q_weight), ("k_weight", self.k_weight)):
+            if w is not None and (w.dim() != 1 or w.shape[0] != head_size):
+                raise ValueError("%s must have head_size entries" % name)
+        for w in (self.q_weight, self.k_weight, None if r is None else r.turns):
+            if w is not None and w.device != device:
+                raise ValueError("the transform's tensors must be on the rows' device")
+        return _QKTransform(_addr(self.q_weight), _addr(self.k_weight), float(self.eps),
+                            None if r is None else r.turns.data_ptr(), 1.0 if r is None else float(r.factor),
+                            0 if r is None else r.rotary_dim, 1 if self.interleaved else 0)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _rows(t, name, tokens=None, heads=None, head_size=None, like=None):
+    """Checks [T, heads, head_size] rows whose tokens may be strided."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3:
+        raise ValueError("%s must be a CUDA tensor [tokens, heads, head_size]" % name)
+    T, n, D = t.shape
+    if (tokens is not None and T != tokens) or (heads is not None and n != heads) or \
+            (head_size is not None and D != head_size):
+        raise ValueError("%s has the wrong shape %s" % (name, tuple(t.shape)))
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise ValueError("%s must have the queries' type and device" % name)
+    if (D > 1 and t.stride(2) != 1) or (n > 1 and t.stride(1) != D):
+        raise ValueError("the heads of a token of %s must be contiguous" % name)
+    # (a single token's stride says nothing)
+    return max(t.stride(0), n * D) if T <= 1 else t.stride(0)
+
+
+def _token_index(t, name, tokens, device):
+    _need(t, name, torch.int64)
+    if t.dim() != 1 or t.shape[0] != tokens or t.device != device:
+        raise ValueError("%s must be int64 [tokens] on the queries' device" % name)
+
+
+def pa_qk_norm_rope(q_out: torch.Tensor, k_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
+                    positions: Optional[torch.Tensor], transform: QKTransform):
+    """Norms and rotates the heads of q [T, num_heads, head_size] and k [T,
+    num_kv_heads, head_size] (tokens may be strided: views of a fused qkv buffer)
+    into q_out and k_out of the same shapes, which may be q and k themselves;
+    positions: int64 [T]."""
+    qs = _rows(q, "q")
+    T, H, D = q.shape
+    ks = _rows(k, "k", T, None, D, q)
+    qos, kos = _rows(q_out, "q_out", T, H, D, q), _rows(k_out, "k_out", T, k.shape[1], D, q)
+    if positions is not None:
+        _token_index(positions, "positions", T, q.device)
+    tr = transform.c_struct(D, q.device)
+    with _on(q.device):
+        st = library().pa_qk_norm_rope(_ptr(q_out), _ptr(k_out), _ptr(q), _ptr(k), torch_dtype_code(q.dtype), T, H,
+                                       k.shape[1], D, qs, ks, qos, kos, _ptr(positions), C.byref(tr), _stream(q))
+    _check(st, "pa_qk_norm_rope")
+
+
+def pa_qk_norm_rope_write(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: KVCache,
+                          positions: Optional[torch.Tensor], slot_mapping: torch.Tensor, transform: QKTransform,
+                          dev_status: Optional[torch.Tensor] = None):
+    """pa_qk_norm_rope with the keys, and the values v as they are, written to
+    slot_mapping's (int64 [T], < 0 skips) slots of the cache."""
+    qs = _rows(q, "q")
+    T, H, D = q.shape
+    Hkv = cache.num_kv_heads
+    if D != cache.head_size or cache.k_cache.device != q.device:
+        raise ValueError("the cache must have the queries' head size and device")
+    ks, vs = _rows(k, "k", T, Hkv, D, q), _rows(v, "v", T, Hkv, D, q)
+    qos = _rows(q_out, "q_out", T, H, D, q)
+    if positions is not None:
+        _token_index(positions, "positions", T, q.device)
+    _token_index(slot_mapping, "slot_mapping", T, q.device)
+    cs, tr = cache.c_struct(), transform.c_struct(D, q.device)
+    with _on(q.device):
+        st = library().pa_qk_norm_rope_write(_ptr(q_out), _ptr(q), _ptr(k), _ptr(v), torch_dtype_code(q.dtype),
+                                             C.byref(cs), T, H, qs, ks, vs, qos, _ptr(positions), _ptr(slot_mapping),
+                                             C.byref(tr), _ptr(dev_status), _stream(q))
+    _check(st, "pa_qk_norm_rope_write")
 
 
 def pa_copy_blocks(cache: KVCache, src_dst_pairs: torch.Tensor, dev_status: Optional[torch.Tensor] = None):
