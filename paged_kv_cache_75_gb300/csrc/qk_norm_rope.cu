@@ -18,10 +18,14 @@
 // sincospif: no table to read, and no position too far.
 //
 // The kernel is bandwidth-bound: 2 bytes in and 2 (or 1) out per element
-// against about 10 instructions.  A row is handled by D/8 lanes with one 16-byte
-// load and store each; a block of 256 threads takes a few tokens (all of their
-// rows), so each token's sines are worked out once per block, in shared memory,
-// while its rows' loads are in flight.
+// against about 10 instructions.  A row is handled by D/8 lanes, one 16-byte
+// load and store each, so a warp takes 2 or 4 heads at a time; a warp's unit is
+// one token, or part of its rows when there are few tokens.  Per unit the warp
+// works out the token's sines (two per lane, exchanged through shared memory)
+// while its first rows are in flight, and folds the norm's weights into them:
+//     out = r (x w cos + x' w' sin),  r = 1 / sqrt(mean(x^2) + eps),
+// with x' the other element of the pair, which is swapped between lanes as the
+// 16-bit input it came as.
 #include <cmath>
 
 #include "common.cuh"
@@ -30,9 +34,11 @@
 namespace pa {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kUnroll = 4;       // rows a lane group loads before it works on the first
-constexpr int kMaxTokens = 32;   // tokens of a block's tile
+constexpr int kWarps = 4;        // units of a block, one a warp
+constexpr int kUnroll = 4;       // rows a lane loads before it works on the first
+constexpr int kBlocks = 6;       // blocks per SM that the registers allow
+constexpr int kUnitsPerSm = 96;  // units wanted per SM
+constexpr int kMinSteps = 2;     // steps of a unit, at least, when a token is split
 constexpr int kPacked = -1;      // keys go to packed rows, there is no cache
 
 struct NormRopeParams {
@@ -52,10 +58,10 @@ struct NormRopeParams {
     int64_t num_tokens;
     int64_t num_slots;
     float eps, rope_factor, k_scale, v_scale;
-    int32_t num_heads, num_kv_heads, rows;  // rows of a token: H + Hkv (+ Hkv values)
+    int32_t num_heads, num_kv_heads;
     int32_t rotary_dim, interleaved, block_size;
-    int32_t tile;    // tokens of a block's tile
-    int32_t splits;  // blocks that share a one-token tile's rows
+    int32_t parts;     // units of a token
+    int32_t per_part;  // steps of a unit (a step: the rows a warp takes at a time)
     // 16-byte accesses allowed (pointer and stride aligned)
     bool q_vec, k_vec, v_vec, qo_vec, ko_vec;
 };
@@ -102,181 +108,235 @@ __device__ __forceinline__ uint2 e4m3_8(const float (&x)[8], float scale) {
     return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
 
-// DT: type of the rows; KVT: kPacked, DT (16-bit cache) or PA_FP8_E4M3
-template <int DT, int KVT, int D>
-__global__ void __launch_bounds__(kThreads)
-qk_norm_rope_kernel(const NormRopeParams p) {
-    constexpr int LPR = D / 8;               // lanes per row, 8 elements each
-    constexpr int GROUPS = kThreads / LPR;   // rows in work at a time
-    __shared__ float2 turn[kMaxTokens][D / 2];  // (cos, sin) * factor of each token and pair
-    __shared__ int64_t cache_row[kMaxTokens];   // row of KV head 0 in the cache, -1: none
-    pdl_wait();
-    pdl_trigger();
-    const int lane = threadIdx.x & 31;
-    const int c = threadIdx.x % LPR;   // this lane's 8-element chunk of its rows
-    const int group = threadIdx.x / LPR;
-    const int half = p.rotary_dim / 16;  // chunks of half the rotated part
-    // half layout: the lane that holds the other element of this lane's pairs
-    const bool rotated = c < 2 * half;
-    const int partner = (lane & ~(LPR - 1)) + (!rotated ? c : c < half ? c + half : c - half);
-    const int pair0 = p.interleaved ? 4 * c : 8 * (c < half ? c : c - half);
-    const float side = c < half ? -1.f : 1.f;  // half layout: sign of the sine's term
+// packed fp32 pairs: one instruction for both halves
+__device__ __forceinline__ uint64_t pair2(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 unpair2(uint64_t r) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(r));
+    return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+template <int DT>
+__device__ __forceinline__ uint64_t widen(uint32_t w) {
+    const float2 f = kv_pair<DT>(w);
+    return pair2(f.x, f.y);
+}
 
-    const int64_t tiles = (p.num_tokens + p.tile - 1) / p.tile;
-    for (int64_t u = blockIdx.x; u < tiles * p.splits; u += gridDim.x) {
-        const int64_t t0 = u / p.splits * p.tile;
-        const int nt = static_cast<int>(min(static_cast<int64_t>(p.tile), p.num_tokens - t0));
-        // rows [r0, r1) of the tile, token-major
-        const int part = static_cast<int>(u % p.splits);
-        const int r0 = part * GROUPS, step = p.splits * GROUPS, r1 = nt * p.rows;
-        bool first = true;
-        for (int base = r0; base < r1; base += step * kUnroll) {
-            uint4 raw[kUnroll];
-            int tok[kUnroll], row[kUnroll];
+// The state of a warp's unit: its token, this lane's place in the rows, the
+// sines once they are worked out.
+struct Unit {
+    int64_t t;     // token
+    int64_t at;    // cache row of the token's KV head 0, -1 for none
+    float2* turn;  // shared memory: (cos, sin) * factor of the token's pairs
+    int c, sub;    // chunk of 8 elements, row of a step
+    int half;      // chunks of half the rotated part
+    int other;     // half layout: chunk that holds the other elements of this lane's pairs
+    bool rotated;
+    bool ready;  // the sines are in `turn`
+};
+
+__device__ __forceinline__ void work_out_sines(const NormRopeParams& p, Unit& u) {
+    if (u.ready || u.half == 0) return;
+    u.ready = true;
+    const uint64_t pos = static_cast<uint64_t>(__ldg(p.positions + u.t));
+    for (int i = threadIdx.x & 31; i < p.rotary_dim / 2; i += 32) {
+        // the signed top half of the phase is the fraction of a turn in units
+        // of 2^-32, so * 2^-31 gives half turns in [-1, 1)
+        const int32_t frac = static_cast<int32_t>((pos * __ldg(p.turns + i)) >> 32);
+        float s, c;
+        sincospif(static_cast<float>(frac) * 4.656612873077393e-10f, &s, &c);
+        u.turn[i] = make_float2(c * p.rope_factor, s * p.rope_factor);
+    }
+    __syncwarp();
+}
+
+// Steps [s0, s1) of the token's queries (KIND 0), keys (1) or values (2).
+template <int DT, int KVT, int D, int KIND>
+__device__ __forceinline__ void do_steps(const NormRopeParams& p, Unit& u, int s0, int s1) {
+    constexpr int LPR = D / 8, RPS = 32 / LPR;
+    if (s0 >= s1) return;
+    const int n = KIND == 0 ? p.num_heads : p.num_kv_heads;
+    const uint16_t* src = (KIND == 0 ? p.q + u.t * p.q_stride : KIND == 1 ? p.k + u.t * p.k_stride
+                                                                          : p.v + u.t * p.v_stride) + u.c * 8;
+    const bool vec = KIND == 0 ? p.q_vec : KIND == 1 ? p.k_vec : p.v_vec;
+    const float* w = KIND == 0 ? p.q_weight : p.k_weight;
+    const bool norm = KIND != 2 && w != nullptr;
+    const int partner = (threadIdx.x & 31 & ~(LPR - 1)) + u.other;
+    uint64_t wc[4], ws[4];  // weight * cos, the other element's weight * signed sin
+    for (int i = s0; i < s1; i += kUnroll) {
+        uint4 raw[kUnroll];
 #pragma unroll
-            for (int j = 0; j < kUnroll; ++j) {
-                const int rr = base + j * step + group;
-                tok[j] = rr < r1 ? (nt == 1 ? 0 : rr / p.rows) : -1;
-                row[j] = rr - tok[j] * p.rows;
-                raw[j] = make_uint4(0u, 0u, 0u, 0u);
-                if (tok[j] >= 0) {
-                    const int64_t t = t0 + tok[j];
-                    const int h = row[j];
-                    if (h < p.num_heads)
-                        raw[j] = load_row8(p.q + t * p.q_stride + h * D + c * 8, p.q_vec);
-                    else if (h < p.num_heads + p.num_kv_heads)
-                        raw[j] = load_row8(p.k + t * p.k_stride + (h - p.num_heads) * D + c * 8, p.k_vec);
-                    else
-                        raw[j] = load_row8(p.v + t * p.v_stride + (h - p.num_heads - p.num_kv_heads) * D + c * 8,
-                                           p.v_vec);
+        for (int j = 0; j < kUnroll; ++j) {
+            const int h = (i + j) * RPS + u.sub;
+            raw[j] = i + j < s1 && h < n ? load_row8(src + h * D, vec) : make_uint4(0u, 0u, 0u, 0u);
+        }
+        if (KIND != 2 && i == s0) {
+            work_out_sines(p, u);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float2 a = make_float2(1.f, 1.f), b = a, f0 = make_float2(1.f, 0.f), f1 = f0;
+                if (norm) {
+                    a = __ldg(reinterpret_cast<const float2*>(w) + 4 * u.c + e);
+                    b = p.interleaved ? make_float2(a.y, a.x)
+                                      : __ldg(reinterpret_cast<const float2*>(w) + 4 * u.other + e);
                 }
-            }
-            if (first) {
-                first = false;
-                const int pairs = p.rotary_dim / 2;
-                for (int i = threadIdx.x; i < nt * pairs; i += kThreads) {
-                    const int tt = nt == 1 ? 0 : i / pairs, pr = i - tt * pairs;
-                    const uint64_t phase = static_cast<uint64_t>(__ldg(p.positions + t0 + tt)) * __ldg(p.turns + pr);
-                    // the signed top half is the fraction of a turn in units of
-                    // 2^-32, so * 2^-31 gives half turns in [-1, 1)
-                    const float x = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f;
-                    float s, co;
-                    sincospif(x, &s, &co);
-                    turn[tt][pr] = make_float2(co * p.rope_factor, s * p.rope_factor);
-                }
-                if constexpr (KVT != kPacked) {
-                    if (threadIdx.x < nt) {
-                        const int64_t slot = __ldg(p.slots + t0 + threadIdx.x);
-                        int64_t at = -1;
-                        if (slot >= p.num_slots) {
-                            report(p.status, PA_ERR_BAD_BLOCK);
-                        } else if (slot >= 0) {
-                            const int64_t blk = slot / p.block_size;
-                            at = blk * p.num_kv_heads * p.block_size + (slot - blk * p.block_size);
-                        }
-                        cache_row[threadIdx.x] = at;
+                if (u.rotated) {
+                    if (p.interleaved) {
+                        f1 = u.turn[4 * u.c + e];
+                        f0 = make_float2(f1.x, -f1.y);
+                    } else {
+                        const bool low = u.c < u.half;
+                        const float4 f = *reinterpret_cast<const float4*>(u.turn + 8 * (low ? u.c : u.c - u.half) + 2 * e);
+                        f0 = make_float2(f.x, low ? -f.y : f.y);
+                        f1 = make_float2(f.z, low ? -f.w : f.w);
                     }
                 }
-                __syncthreads();
+                wc[e] = pair2(a.x * f0.x, a.y * f1.x);
+                ws[e] = pair2(b.x * f0.y, b.y * f1.y);
             }
+        }
 #pragma unroll
-            for (int j = 0; j < kUnroll; ++j) {
-                const bool is_q = row[j] < p.num_heads;
-                const bool is_v = row[j] >= p.num_heads + p.num_kv_heads;
-                const int tt = tok[j] < 0 ? 0 : tok[j];
-                const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
-                float y[8];
+        for (int j = 0; j < kUnroll; ++j) {
+            if (i + j >= s1) break;
+            uint32_t x[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+            uint64_t o[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 f = kv_pair<DT>(w[e]);
-                    y[2 * e] = f.x;
-                    y[2 * e + 1] = f.y;
-                }
-                const float* wt = is_q ? p.q_weight : p.k_weight;
-                if (p.q_weight != nullptr || p.k_weight != nullptr) {
-                    float ss = 0.f;
+            for (int e = 0; e < 4; ++e) o[e] = widen<DT>(x[e]);
+            if constexpr (KIND != 2) {
+                uint64_t z[4];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
+                for (int e = 0; e < 4; ++e)
+                    z[e] = widen<DT>(p.interleaved ? __byte_perm(x[e], 0u, 0x1032)
+                                                   : __shfl_sync(0xffffffffu, x[e], partner));
+                float r = 1.f;
+                if (norm) {
+                    uint64_t s2 = mul2(o[0], o[0]);
 #pragma unroll
-                    for (int o = 1; o < LPR; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                    float r = rsqrtf(fmaf(ss, 1.f / D, p.eps));
+                    for (int e = 1; e < 4; ++e) s2 = fma2(o[e], o[e], s2);
+                    const float2 sp = unpair2(s2);
+                    float ss = sp.x + sp.y;
+#pragma unroll
+                    for (int d = 1; d < LPR; d <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+                    r = rsqrtf(fmaf(ss, 1.f / D, p.eps));
                     // squares past fp32's range (bf16 rows beyond 10^18): again
                     // on the row scaled by 2^-70, next to which eps is nothing
                     const bool big = !(ss < INFINITY);
                     if (__any_sync(0xffffffffu, big)) {
                         const float down = big ? 8.470329472543003e-22f : 1.f;
-                        float s2 = 0.f;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) s2 = fmaf(y[e] * down, y[e] * down, s2);
-#pragma unroll
-                        for (int o = 1; o < LPR; o <<= 1) s2 += __shfl_xor_sync(0xffffffffu, s2, o);
-                        if (big) {
-                            r = rsqrtf(s2 * (1.f / D));
-                            if (wt != nullptr && !is_v) {
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) y[e] *= down;
-                            }
-                        }
-                    }
-                    if (wt != nullptr && !is_v) {
-                        const float4 w0 = __ldg(reinterpret_cast<const float4*>(wt) + 2 * c);
-                        const float4 w1 = __ldg(reinterpret_cast<const float4*>(wt) + 2 * c + 1);
-                        y[0] *= r * w0.x; y[1] *= r * w0.y; y[2] *= r * w0.z; y[3] *= r * w0.w;
-                        y[4] *= r * w1.x; y[5] *= r * w1.y; y[6] *= r * w1.z; y[7] *= r * w1.w;
-                    }
-                }
-                if (p.interleaved) {
-                    if (rotated && !is_v) {
+                        const uint64_t d2 = pair2(down, down);
+                        float sb = 0.f;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float2 t = turn[tt][pair0 + e];
-                            const float a = y[2 * e], b = y[2 * e + 1];
-                            y[2 * e] = fmaf(a, t.x, -(b * t.y));
-                            y[2 * e + 1] = fmaf(b, t.x, a * t.y);
+                            o[e] = mul2(o[e], d2);
+                            z[e] = mul2(z[e], d2);
+                            const float2 f = unpair2(o[e]);
+                            sb = fmaf(f.x, f.x, fmaf(f.y, f.y, sb));
                         }
-                    }
-                } else if (half > 0) {
-                    float z[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) z[e] = __shfl_sync(0xffffffffu, y[e], partner);
-                    if (rotated && !is_v) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float2 t = turn[tt][pair0 + e];
-                            y[e] = fmaf(y[e], t.x, side * (z[e] * t.y));
-                        }
+                        for (int d = 1; d < LPR; d <<= 1) sb += __shfl_xor_sync(0xffffffffu, sb, d);
+                        if (big) r = rsqrtf(sb * (1.f / D));
                     }
                 }
-                if (tok[j] < 0) continue;
-                const int64_t t = t0 + tok[j];
-                // values, and rows that nothing changed, keep their bits
-                const bool same = is_v || (wt == nullptr && !rotated);
-                uint4 x = raw[j];
-                if (!same)
-                    x = make_uint4(round_pair<DT>(y[0], y[1]), round_pair<DT>(y[2], y[3]), round_pair<DT>(y[4], y[5]),
-                                   round_pair<DT>(y[6], y[7]));
-                if (is_q) {
-                    store_row8(p.q_out + t * p.qo_stride + row[j] * D + c * 8, x, p.qo_vec);
-                    continue;
+                const uint64_t r2 = pair2(r, r);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    // an element that nothing turns takes no part of another (which may be infinite)
+                    o[e] = mul2(o[e], wc[e]);
+                    if (u.rotated) o[e] = fma2(z[e], ws[e], o[e]);
+                    if (norm) o[e] = mul2(o[e], r2);
                 }
-                const int h = row[j] - p.num_heads - (is_v ? p.num_kv_heads : 0);
-                if constexpr (KVT == kPacked) {
-                    store_row8(static_cast<uint16_t*>(p.k_out) + t * p.ko_stride + h * D + c * 8, x, p.ko_vec);
+            }
+            const int h = (i + j) * RPS + u.sub;
+            if (h >= n) continue;
+            uint4 out = raw[j];
+            // (elements that nothing changed keep their bits)
+            if (KIND != 2 && (norm || u.rotated)) {
+                uint32_t y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 f = unpair2(o[e]);
+                    y[e] = round_pair<DT>(f.x, f.y);
+                }
+                out = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+            if constexpr (KIND == 0) {
+                store_row8(p.q_out + u.t * p.qo_stride + h * D + u.c * 8, out, p.qo_vec);
+            } else if constexpr (KVT == kPacked) {
+                store_row8(static_cast<uint16_t*>(p.k_out) + u.t * p.ko_stride + h * D + u.c * 8, out, p.ko_vec);
+            } else if (u.at >= 0) {
+                const int64_t off = (u.at + static_cast<int64_t>(h) * p.block_size) * D + u.c * 8;
+                void* dst = KIND == 2 ? p.v_out : p.k_out;
+                if constexpr (KVT == PA_FP8_E4M3) {
+                    float f[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 g = unpair2(o[e]);
+                        f[2 * e] = g.x;
+                        f[2 * e + 1] = g.y;
+                    }
+                    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(dst) + off) =
+                        e4m3_8(f, KIND == 2 ? p.v_scale : p.k_scale);
                 } else {
-                    const int64_t at = cache_row[tt];
-                    if (at < 0) continue;
-                    const int64_t off = (at + static_cast<int64_t>(h) * p.block_size) * D + c * 8;
-                    void* dst = is_v ? p.v_out : p.k_out;
-                    if constexpr (KVT == PA_FP8_E4M3)
-                        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(dst) + off) =
-                            e4m3_8(y, is_v ? p.v_scale : p.k_scale);
-                    else
-                        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + off) = x;
+                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + off) = out;
                 }
             }
         }
-        __syncthreads();  // the next tile writes the sines again
     }
+}
+
+// DT: type of the rows; KVT: kPacked, DT (16-bit cache) or PA_FP8_E4M3
+template <int DT, int KVT, int D>
+__global__ void __launch_bounds__(kWarps * 32, kBlocks)
+qk_norm_rope_kernel(const NormRopeParams p) {
+    constexpr int LPR = D / 8;      // lanes per row, 8 elements each
+    constexpr int RPS = 32 / LPR;   // rows of a step
+    __shared__ __align__(16) float2 turn_all[kWarps][D / 2];
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+    if (unit >= p.num_tokens * p.parts) return;
+    Unit u;
+    u.t = p.parts == 1 ? unit : unit / p.parts;
+    u.turn = turn_all[warp];
+    u.c = lane % LPR;
+    u.sub = lane / LPR;
+    u.half = p.rotary_dim / 16;
+    u.rotated = u.c < 2 * u.half;
+    u.other = p.interleaved || !u.rotated ? u.c : (u.c < u.half ? u.c + u.half : u.c - u.half);
+    u.ready = false;
+    u.at = -1;
+
+    // the token's steps: queries, keys, values; this unit takes [i0, i1)
+    const int qs = (p.num_heads + RPS - 1) / RPS, ks = (p.num_kv_heads + RPS - 1) / RPS;
+    const int i0 = static_cast<int>(unit - u.t * p.parts) * p.per_part, i1 = i0 + p.per_part;
+    if (KVT != kPacked && i1 > qs) {
+        const int64_t slot = __ldg(p.slots + u.t);
+        if (slot >= p.num_slots) {
+            if (lane == 0) report(p.status, PA_ERR_BAD_BLOCK);
+        } else if (slot >= 0) {
+            // (a 32-bit division where it does: a 64-bit one is ten times as long)
+            const int64_t blk = slot >> 32 == 0 ? static_cast<uint32_t>(slot) / static_cast<uint32_t>(p.block_size)
+                                                : slot / p.block_size;
+            u.at = blk * p.num_kv_heads * p.block_size + (slot - blk * p.block_size);
+        }
+    }
+    do_steps<DT, KVT, D, 0>(p, u, i0, min(i1, qs));
+    do_steps<DT, KVT, D, 1>(p, u, max(i0 - qs, 0), min(i1 - qs, ks));
+    if constexpr (KVT != kPacked) do_steps<DT, KVT, D, 2>(p, u, max(i0 - qs - ks, 0), min(i1 - qs - ks, ks));
 }
 
 bool aligned16(const void* ptr, int64_t stride) {
@@ -285,25 +345,24 @@ bool aligned16(const void* ptr, int64_t stride) {
 
 template <int DT, int KVT, int D>
 pa_status launch_t(NormRopeParams p, cudaStream_t stream) {
-    constexpr int GROUPS = kThreads / (D / 8);
+    constexpr int RPS = 32 / (D / 8);
     const int64_t sms = device_sm_count();
     if (sms <= 0) return PA_ERR_CUDA;
-    // a tile of about kUnroll rows per lane group; fewer tokens when they would
-    // leave SMs without a tile, and a token's rows over several blocks when
-    // there are fewer tokens than SMs
-    int64_t tile = GROUPS * kUnroll / p.rows;
-    if (tile > p.num_tokens / sms) tile = p.num_tokens / sms;
-    p.tile = static_cast<int32_t>(tile < 1 ? 1 : (tile > kMaxTokens ? kMaxTokens : tile));
-    const int64_t most = (p.rows + GROUPS - 1) / GROUPS;
-    p.splits = 1;
-    if (p.tile == 1 && p.num_tokens < sms) {
-        const int64_t want = sms / p.num_tokens;
-        p.splits = static_cast<int32_t>(want < most ? want : most);
-    }
-    const int64_t units = (p.num_tokens + p.tile - 1) / p.tile * p.splits;
-    const int grid = static_cast<int>(units < INT32_MAX ? units : INT32_MAX);
-    return launch_pdl(qk_norm_rope_kernel<DT, KVT, D>, grid, kThreads, 0, stream, p) == cudaSuccess ? PA_OK
-                                                                                                   : PA_ERR_CUDA;
+    const int ks = (p.num_kv_heads + RPS - 1) / RPS;
+    const int steps = (p.num_heads + RPS - 1) / RPS + ks * (KVT == kPacked ? 1 : 2);
+    // units of a token: one (its sines are worked out once), more while the
+    // units would not fill the SMs' warps a few times over
+    const int64_t want = sms * kUnitsPerSm / p.num_tokens;
+    const int64_t most = (steps + kMinSteps - 1) / kMinSteps;
+    const int parts = static_cast<int>(want < 1 ? 1 : (want < most ? want : most));
+    p.per_part = (steps + parts - 1) / parts;
+    p.parts = (steps + p.per_part - 1) / p.per_part;
+    const int64_t blocks = (p.num_tokens * p.parts + kWarps - 1) / kWarps;
+    if (blocks > INT32_MAX) return PA_ERR_UNSUPPORTED;
+    return launch_pdl(qk_norm_rope_kernel<DT, KVT, D>, static_cast<int>(blocks), kWarps * 32, 0, stream, p) ==
+                   cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
 }
 
 pa_status launch(const NormRopeParams& p, int dt, int kvt, int head_size, cudaStream_t s) {
@@ -384,7 +443,6 @@ extern "C" pa_status pa_qk_norm_rope(void* q_out, void* k_out, const void* q, co
     p.k_out = k_out;
     p.ko_stride = k_out_stride;
     p.ko_vec = aligned16(k_out, k_out_stride);
-    p.rows = num_heads + num_kv_heads;
     return launch(p, dtype, kPacked, head_size, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -419,7 +477,6 @@ extern "C" pa_status pa_qk_norm_rope_write(void* q_out, const void* q, const voi
     p.num_slots = cache->num_blocks * cache->block_size;
     p.k_scale = cache->k_scale;
     p.v_scale = cache->v_scale;
-    p.rows = num_heads + 2 * cache->num_kv_heads;
     return launch(p, dtype, fp8 ? PA_FP8_E4M3 : static_cast<int>(dtype), cache->head_size,
                   reinterpret_cast<cudaStream_t>(stream));
 }
