@@ -17,15 +17,23 @@
 // frequency wraps to the exact fraction of a turn, whose top 32 bits go to
 // sincospif: no table to read, and no position too far.
 //
-// The kernel is bandwidth-bound: 2 bytes in and 2 (or 1) out per element
-// against about 10 instructions.  A row is handled by D/8 lanes, one 16-byte
-// load and store each, so a warp takes 2 or 4 heads at a time; a warp's unit is
-// one token, or part of its rows when there are few tokens.  Per unit the warp
-// works out the token's sines (two per lane, exchanged through shared memory)
-// while its first rows are in flight, and folds the norm's weights into them:
+// The kernel is bandwidth-bound (2 bytes in and 2 or 1 out per element) as long
+// as it spends few instructions on an element: a first version with 8 elements
+// a lane took 172 instructions for 256 elements and was bound by their issue
+// at 70 % of the copy rate.  So D/16 lanes share a row, two 16-byte chunks a
+// lane, chosen so that a lane holds both elements of its pairs: chunks j and j +
+// rotary_dim/16 in the half layout (the lanes past the rotated part share the
+// rest), whole pairs in any chunk when interleaved.  No element changes lanes,
+// the sum of squares is all that does.  A warp takes a step of 4 heads (8 of
+// 64 elements) at a time.  The call's steps (all tokens' queries, keys, values)
+// are dealt out to the resident warps in equal contiguous runs.  Each lane keeps
+// the next rows in flight through a ring of its own in shared memory (16-byte
+// asynchronous copies that only the same lane reads back: no barrier, and no
+// register held while a load is on its way).  When a run enters a token, the warp
+// works out its sines (two per lane, exchanged through shared memory) and folds
+// the norm's weights into them:
 //     out = r (x w cos + x' w' sin),  r = 1 / sqrt(mean(x^2) + eps),
-// with x' the other element of the pair, which is swapped between lanes as the
-// 16-bit input it came as.
+// with x' the other element of the pair.
 #include <cmath>
 
 #include "common.cuh"
@@ -34,12 +42,11 @@
 namespace pa {
 namespace {
 
-constexpr int kWarps = 4;        // units of a block, one a warp
-constexpr int kUnroll = 4;       // rows a lane loads before it works on the first
-constexpr int kBlocks = 6;       // blocks per SM that the registers allow
-constexpr int kUnitsPerSm = 96;  // units wanted per SM
-constexpr int kMinSteps = 2;     // steps of a unit, at least, when a token is split
-constexpr int kPacked = -1;      // keys go to packed rows, there is no cache
+constexpr int kWarps = 4;     // warps of a block
+constexpr int kBlocks = 5;    // blocks per SM that the registers allow
+constexpr int kDepth = 8;     // steps a lane's ring holds
+constexpr int kMinSteps = 1;  // steps of a warp's run, at least
+constexpr int kPacked = -1;   // keys go to packed rows, there is no cache
 
 struct NormRopeParams {
     const uint16_t* q;
@@ -60,14 +67,13 @@ struct NormRopeParams {
     float eps, rope_factor, k_scale, v_scale;
     int32_t num_heads, num_kv_heads;
     int32_t rotary_dim, interleaved, block_size;
-    int32_t parts;     // units of a token
-    int32_t per_part;  // steps of a unit (a step: the rows a warp takes at a time)
+    int64_t per_warp, extra;  // steps of a warp's run: per_warp, one more for the first `extra` warps
     // 16-byte accesses allowed (pointer and stride aligned)
     bool q_vec, k_vec, v_vec, qo_vec, ko_vec;
 };
 
-__device__ __forceinline__ uint4 load_row8(const uint16_t* p, bool vec) {
-    if (vec) return __ldcs(reinterpret_cast<const uint4*>(p));
+// 16 bytes of a row that is not 16-byte aligned
+__device__ __forceinline__ uint4 load_odd8(const uint16_t* p) {
     uint32_t w[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) w[j] = static_cast<uint32_t>(p[2 * j]) | static_cast<uint32_t>(p[2 * j + 1]) << 16;
@@ -98,16 +104,6 @@ __device__ __forceinline__ uint32_t round_pair(float a, float b) {
     }
 }
 
-// 8 values -> 8 E4M3 codes: IEEE division, then one rounding with saturation
-__device__ __forceinline__ uint2 e4m3_8(const float (&x)[8], float scale) {
-    uint32_t c[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        c[j] = static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(
-            make_float2(__fdiv_rn(x[2 * j], scale), __fdiv_rn(x[2 * j + 1], scale)), __NV_SATFINITE, __NV_E4M3));
-    return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
-}
-
 // packed fp32 pairs: one instruction for both halves
 __device__ __forceinline__ uint64_t pair2(float x, float y) {
     uint64_t r;
@@ -129,33 +125,121 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
 template <int DT>
 __device__ __forceinline__ uint64_t widen(uint32_t w) {
     const float2 f = kv_pair<DT>(w);
     return pair2(f.x, f.y);
 }
 
-// The state of a warp's unit: its token, this lane's place in the rows, the
-// sines once they are worked out.
-struct Unit {
-    int64_t t;     // token
-    int64_t at;    // cache row of the token's KV head 0, -1 for none
-    float2* turn;  // shared memory: (cos, sin) * factor of the token's pairs
-    int c, sub;    // chunk of 8 elements, row of a step
-    int half;      // chunks of half the rotated part
-    int other;     // half layout: chunk that holds the other elements of this lane's pairs
-    bool rotated;
-    bool ready;  // the sines are in `turn`
+// 8 values (packed pairs) -> 8 E4M3 codes: IEEE division, then one rounding with saturation
+__device__ __forceinline__ uint2 e4m3_8(const uint64_t* x, float scale) {
+    uint32_t c[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 f = unpair2(x[j]);
+        c[j] = static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(
+            make_float2(__fdiv_rn(f.x, scale), __fdiv_rn(f.y, scale)), __NV_SATFINITE, __NV_E4M3));
+    }
+    return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+}
+template <int DT>
+__device__ __forceinline__ uint4 round_8(const uint64_t* x) {
+    uint32_t y[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 f = unpair2(x[j]);
+        y[j] = round_pair<DT>(f.x, f.y);
+    }
+    return make_uint4(y[0], y[1], y[2], y[3]);
+}
+
+// The rows that a warp's run loads: a cursor over (token, segment, step), the
+// segments of a token being its queries (0), keys (1) and values (2).
+template <int KVT, int D>
+struct Loader {
+    static constexpr int RPS = 512 / D;  // rows of a step
+    static constexpr int kSegs = KVT == kPacked ? 2 : 3;
+    const uint16_t* src;  // this lane's first chunk of the step's row
+    int64_t t;
+    int64_t left;  // steps of the run not yet issued
+    int rows;      // rows of the segment from this lane's on
+    int seg;
+    bool vec;
+
+    __device__ __forceinline__ void enter(const NormRopeParams& p, int step, int sub, int c0) {
+        const uint16_t* base = seg == 0 ? p.q + t * p.q_stride : seg == 1 ? p.k + t * p.k_stride : p.v + t * p.v_stride;
+        vec = seg == 0 ? p.q_vec : seg == 1 ? p.k_vec : p.v_vec;
+        rows = (seg == 0 ? p.num_heads : p.num_kv_heads) - step * RPS - sub;
+        src = base + (step * RPS + sub) * D + c0 * 8;
+    }
+    // starts the copies of the next step's row into `slot` and slot[32] (one
+    // group of asynchronous copies a step, empty past the run's end); the second
+    // chunk is `gap` elements after the first
+    __device__ __forceinline__ void issue(const NormRopeParams& p, uint4* slot, int sub, int c0, int gap) {
+        if (left > 0) {
+            const bool have = rows > 0;
+            if (vec) {
+                const uint16_t* from = have ? src : p.q;
+                const uint32_t n = have ? 16u : 0u;
+                asm volatile(
+                    "cp.async.cg.shared.global [%0], [%1], 16, %3;\n\t"
+                    "cp.async.cg.shared.global [%0 + 512], [%2], 16, %3;" ::"r"(smem_addr(slot)),
+                    "l"(reinterpret_cast<uint64_t>(from)), "l"(reinterpret_cast<uint64_t>(have ? src + gap : p.q)), "r"(n)
+                    : "memory");
+            } else {
+                slot[0] = have ? load_odd8(src) : make_uint4(0u, 0u, 0u, 0u);
+                slot[32] = have ? load_odd8(src + gap) : make_uint4(0u, 0u, 0u, 0u);
+            }
+            --left;
+            src += RPS * D;
+            rows -= RPS;
+            // (the segment's last step: no row is left for the step's first lanes)
+            if (rows + sub <= 0 && left > 0) {
+                if (++seg == kSegs) {
+                    seg = 0;
+                    ++t;
+                }
+                enter(p, 0, sub, c0);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
 };
 
-__device__ __forceinline__ void work_out_sines(const NormRopeParams& p, Unit& u) {
+// What a warp's run works on: its token, this lane's place in the rows, the
+// ring, the token's sines once they are worked out.
+template <int KVT, int D>
+struct Run {
+    Loader<KVT, D> load;
+    uint4* ring;      // [kDepth][2][32], this lane's slots
+    int slot;         // of the step to work on
+    int64_t t;
+    int64_t at;       // cache row of the token's KV head 0, -1 for none
+    float2* turn;     // shared memory: (cos, sin) * factor of the token's pairs
+    int64_t pos, next_pos;
+    int64_t next_slot;
+    int sub;          // row of a step
+    int c0, gap;      // first chunk of 8 elements; elements from it to the second
+    int half;         // chunks of half the rotated part
+    bool turned0, turned1;  // the chunks lie in the rotated part
+    bool ready;       // the sines are in `turn`
+};
+
+// (cos, sin) of the token's pairs into shared memory, once a token
+template <int KVT, int D>
+__device__ __forceinline__ void work_out_sines(const NormRopeParams& p, Run<KVT, D>& u) {
     if (u.ready || u.half == 0) return;
     u.ready = true;
-    const uint64_t pos = static_cast<uint64_t>(__ldg(p.positions + u.t));
+    __syncwarp();  // (the token before may still be read)
     for (int i = threadIdx.x & 31; i < p.rotary_dim / 2; i += 32) {
         // the signed top half of the phase is the fraction of a turn in units
         // of 2^-32, so * 2^-31 gives half turns in [-1, 1)
-        const int32_t frac = static_cast<int32_t>((pos * __ldg(p.turns + i)) >> 32);
+        const int32_t frac = static_cast<int32_t>((static_cast<uint64_t>(u.pos) * __ldg(p.turns + i)) >> 32);
         float s, c;
         sincospif(static_cast<float>(frac) * 4.656612873077393e-10f, &s, &c);
         u.turn[i] = make_float2(c * p.rope_factor, s * p.rope_factor);
@@ -163,170 +247,20 @@ __device__ __forceinline__ void work_out_sines(const NormRopeParams& p, Unit& u)
     __syncwarp();
 }
 
-// Steps [s0, s1) of the token's queries (KIND 0), keys (1) or values (2).
-template <int DT, int KVT, int D, int KIND>
-__device__ __forceinline__ void do_steps(const NormRopeParams& p, Unit& u, int s0, int s1) {
-    constexpr int LPR = D / 8, RPS = 32 / LPR;
-    if (s0 >= s1) return;
-    const int n = KIND == 0 ? p.num_heads : p.num_kv_heads;
-    const uint16_t* src = (KIND == 0 ? p.q + u.t * p.q_stride : KIND == 1 ? p.k + u.t * p.k_stride
-                                                                          : p.v + u.t * p.v_stride) + u.c * 8;
-    const bool vec = KIND == 0 ? p.q_vec : KIND == 1 ? p.k_vec : p.v_vec;
-    const float* w = KIND == 0 ? p.q_weight : p.k_weight;
-    const bool norm = KIND != 2 && w != nullptr;
-    const int partner = (threadIdx.x & 31 & ~(LPR - 1)) + u.other;
-    uint64_t wc[4], ws[4];  // weight * cos, the other element's weight * signed sin
-    for (int i = s0; i < s1; i += kUnroll) {
-        uint4 raw[kUnroll];
-#pragma unroll
-        for (int j = 0; j < kUnroll; ++j) {
-            const int h = (i + j) * RPS + u.sub;
-            raw[j] = i + j < s1 && h < n ? load_row8(src + h * D, vec) : make_uint4(0u, 0u, 0u, 0u);
-        }
-        if (KIND != 2 && i == s0) {
-            work_out_sines(p, u);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float2 a = make_float2(1.f, 1.f), b = a, f0 = make_float2(1.f, 0.f), f1 = f0;
-                if (norm) {
-                    a = __ldg(reinterpret_cast<const float2*>(w) + 4 * u.c + e);
-                    b = p.interleaved ? make_float2(a.y, a.x)
-                                      : __ldg(reinterpret_cast<const float2*>(w) + 4 * u.other + e);
-                }
-                if (u.rotated) {
-                    if (p.interleaved) {
-                        f1 = u.turn[4 * u.c + e];
-                        f0 = make_float2(f1.x, -f1.y);
-                    } else {
-                        const bool low = u.c < u.half;
-                        const float4 f = *reinterpret_cast<const float4*>(u.turn + 8 * (low ? u.c : u.c - u.half) + 2 * e);
-                        f0 = make_float2(f.x, low ? -f.y : f.y);
-                        f1 = make_float2(f.z, low ? -f.w : f.w);
-                    }
-                }
-                wc[e] = pair2(a.x * f0.x, a.y * f1.x);
-                ws[e] = pair2(b.x * f0.y, b.y * f1.y);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < kUnroll; ++j) {
-            if (i + j >= s1) break;
-            uint32_t x[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
-            uint64_t o[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = widen<DT>(x[e]);
-            if constexpr (KIND != 2) {
-                uint64_t z[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    z[e] = widen<DT>(p.interleaved ? __byte_perm(x[e], 0u, 0x1032)
-                                                   : __shfl_sync(0xffffffffu, x[e], partner));
-                float r = 1.f;
-                if (norm) {
-                    uint64_t s2 = mul2(o[0], o[0]);
-#pragma unroll
-                    for (int e = 1; e < 4; ++e) s2 = fma2(o[e], o[e], s2);
-                    const float2 sp = unpair2(s2);
-                    float ss = sp.x + sp.y;
-#pragma unroll
-                    for (int d = 1; d < LPR; d <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-                    r = rsqrtf(fmaf(ss, 1.f / D, p.eps));
-                    // squares past fp32's range (bf16 rows beyond 10^18): again
-                    // on the row scaled by 2^-70, next to which eps is nothing
-                    const bool big = !(ss < INFINITY);
-                    if (__any_sync(0xffffffffu, big)) {
-                        const float down = big ? 8.470329472543003e-22f : 1.f;
-                        const uint64_t d2 = pair2(down, down);
-                        float sb = 0.f;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            o[e] = mul2(o[e], d2);
-                            z[e] = mul2(z[e], d2);
-                            const float2 f = unpair2(o[e]);
-                            sb = fmaf(f.x, f.x, fmaf(f.y, f.y, sb));
-                        }
-#pragma unroll
-                        for (int d = 1; d < LPR; d <<= 1) sb += __shfl_xor_sync(0xffffffffu, sb, d);
-                        if (big) r = rsqrtf(sb * (1.f / D));
-                    }
-                }
-                const uint64_t r2 = pair2(r, r);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    // an element that nothing turns takes no part of another (which may be infinite)
-                    o[e] = mul2(o[e], wc[e]);
-                    if (u.rotated) o[e] = fma2(z[e], ws[e], o[e]);
-                    if (norm) o[e] = mul2(o[e], r2);
-                }
-            }
-            const int h = (i + j) * RPS + u.sub;
-            if (h >= n) continue;
-            uint4 out = raw[j];
-            // (elements that nothing changed keep their bits)
-            if (KIND != 2 && (norm || u.rotated)) {
-                uint32_t y[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 f = unpair2(o[e]);
-                    y[e] = round_pair<DT>(f.x, f.y);
-                }
-                out = make_uint4(y[0], y[1], y[2], y[3]);
-            }
-            if constexpr (KIND == 0) {
-                store_row8(p.q_out + u.t * p.qo_stride + h * D + u.c * 8, out, p.qo_vec);
-            } else if constexpr (KVT == kPacked) {
-                store_row8(static_cast<uint16_t*>(p.k_out) + u.t * p.ko_stride + h * D + u.c * 8, out, p.ko_vec);
-            } else if (u.at >= 0) {
-                const int64_t off = (u.at + static_cast<int64_t>(h) * p.block_size) * D + u.c * 8;
-                void* dst = KIND == 2 ? p.v_out : p.k_out;
-                if constexpr (KVT == PA_FP8_E4M3) {
-                    float f[8];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 g = unpair2(o[e]);
-                        f[2 * e] = g.x;
-                        f[2 * e + 1] = g.y;
-                    }
-                    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(dst) + off) =
-                        e4m3_8(f, KIND == 2 ? p.v_scale : p.k_scale);
-                } else {
-                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + off) = out;
-                }
-            }
-        }
-    }
-}
-
-// DT: type of the rows; KVT: kPacked, DT (16-bit cache) or PA_FP8_E4M3
-template <int DT, int KVT, int D>
-__global__ void __launch_bounds__(kWarps * 32, kBlocks)
-qk_norm_rope_kernel(const NormRopeParams p) {
-    constexpr int LPR = D / 8;      // lanes per row, 8 elements each
-    constexpr int RPS = 32 / LPR;   // rows of a step
-    __shared__ __align__(16) float2 turn_all[kWarps][D / 2];
-    pdl_wait();
-    pdl_trigger();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
-    if (unit >= p.num_tokens * p.parts) return;
-    Unit u;
-    u.t = p.parts == 1 ? unit : unit / p.parts;
-    u.turn = turn_all[warp];
-    u.c = lane % LPR;
-    u.sub = lane / LPR;
-    u.half = p.rotary_dim / 16;
-    u.rotated = u.c < 2 * u.half;
-    u.other = p.interleaved || !u.rotated ? u.c : (u.c < u.half ? u.c + u.half : u.c - u.half);
+// The token's position and its slot's place in the cache (loaded a token ahead).
+template <int KVT, int D>
+__device__ __forceinline__ void enter_token(const NormRopeParams& p, Run<KVT, D>& u) {
     u.ready = false;
-    u.at = -1;
-
-    // the token's steps: queries, keys, values; this unit takes [i0, i1)
-    const int qs = (p.num_heads + RPS - 1) / RPS, ks = (p.num_kv_heads + RPS - 1) / RPS;
-    const int i0 = static_cast<int>(unit - u.t * p.parts) * p.per_part, i1 = i0 + p.per_part;
-    if (KVT != kPacked && i1 > qs) {
-        const int64_t slot = __ldg(p.slots + u.t);
+    u.pos = u.next_pos;
+    const int64_t slot = u.next_slot;
+    if (u.t + 1 < p.num_tokens) {
+        if (u.half > 0) u.next_pos = __ldg(p.positions + u.t + 1);
+        if (KVT != kPacked) u.next_slot = __ldg(p.slots + u.t + 1);
+    }
+    if (KVT != kPacked) {
+        u.at = -1;
         if (slot >= p.num_slots) {
-            if (lane == 0) report(p.status, PA_ERR_BAD_BLOCK);
+            if ((threadIdx.x & 31) == 0) report(p.status, PA_ERR_BAD_BLOCK);
         } else if (slot >= 0) {
             // (a 32-bit division where it does: a 64-bit one is ten times as long)
             const int64_t blk = slot >> 32 == 0 ? static_cast<uint32_t>(slot) / static_cast<uint32_t>(p.block_size)
@@ -334,32 +268,241 @@ qk_norm_rope_kernel(const NormRopeParams p) {
             u.at = blk * p.num_kv_heads * p.block_size + (slot - blk * p.block_size);
         }
     }
-    do_steps<DT, KVT, D, 0>(p, u, i0, min(i1, qs));
-    do_steps<DT, KVT, D, 1>(p, u, max(i0 - qs, 0), min(i1 - qs, ks));
-    if constexpr (KVT != kPacked) do_steps<DT, KVT, D, 2>(p, u, max(i0 - qs - ks, 0), min(i1 - qs - ks, ks));
+}
+
+// wc: weight * cos of this lane's 16 elements; ws: the weight of the other
+// element of each pair * the sine with its sign in this one
+template <bool INTER>
+__device__ __forceinline__ void fold(const float* w, const float2* turn, int c0, int gap, bool turned0, bool turned1,
+                                     uint64_t (&wc)[8], uint64_t (&ws)[8]) {
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {  // pairs of elements of both chunks
+        float2 a = make_float2(1.f, 1.f), b = a;
+        if (w != nullptr) {
+            a = __ldg(reinterpret_cast<const float2*>(w + 8 * c0) + h);
+            b = __ldg(reinterpret_cast<const float2*>(w + 8 * c0 + gap) + h);
+        }
+        if constexpr (INTER) {
+            float2 f = turned0 ? turn[4 * c0 + h] : make_float2(1.f, 0.f);
+            wc[h] = pair2(a.x * f.x, a.y * f.x);
+            ws[h] = pair2(a.y * -f.y, a.x * f.y);
+            f = turned1 ? turn[4 * c0 + gap / 2 + h] : make_float2(1.f, 0.f);
+            wc[4 + h] = pair2(b.x * f.x, b.y * f.x);
+            ws[4 + h] = pair2(b.y * -f.y, b.x * f.y);
+        } else {
+            float4 f = make_float4(1.f, 0.f, 1.f, 0.f);
+            if (turned0) f = *reinterpret_cast<const float4*>(turn + 8 * c0 + 2 * h);
+            wc[h] = pair2(a.x * f.x, a.y * f.z);
+            ws[h] = pair2(b.x * -f.y, b.y * -f.w);
+            wc[4 + h] = pair2(b.x * f.x, b.y * f.z);
+            ws[4 + h] = pair2(a.x * f.y, a.y * f.w);
+        }
+    }
+}
+
+// Steps [s0, s0 + n) of the token's queries (KIND 0), keys (1) or values (2).
+template <int DT, int KVT, int D, bool INTER, int KIND, bool NORM>
+__device__ __forceinline__ void do_steps(const NormRopeParams& p, Run<KVT, D>& u, int s0, int n) {
+    constexpr int LPR = D / 16, RPS = 32 / LPR;
+    constexpr int ES = KIND != 0 && KVT == PA_FP8_E4M3 ? 1 : 2;  // bytes of an output element
+    uint64_t wc[8], ws[8];
+    if constexpr (KIND != 2) {
+        work_out_sines(p, u);
+        fold<INTER>(NORM ? (KIND == 0 ? p.q_weight : p.k_weight) : nullptr, u.turn, u.c0, u.gap, u.turned0, u.turned1,
+                    wc, ws);
+    }
+    // this lane's first chunk of the output, and the way to the next step's
+    uint8_t* dst;
+    int64_t way;
+    int rows = (KIND == 0 ? p.num_heads : p.num_kv_heads) - s0 * RPS - u.sub;
+    const int64_t h0 = s0 * RPS + u.sub;
+    if constexpr (KIND == 0) {
+        dst = reinterpret_cast<uint8_t*>(p.q_out + u.t * p.qo_stride + h0 * D + u.c0 * 8);
+        way = RPS * D * 2;
+    } else if constexpr (KVT == kPacked) {
+        dst = reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(p.k_out) + u.t * p.ko_stride + h0 * D + u.c0 * 8);
+        way = RPS * D * 2;
+    } else {
+        dst = static_cast<uint8_t*>(KIND == 2 ? p.v_out : p.k_out) + ((u.at + h0 * p.block_size) * D + u.c0 * 8) * ES;
+        way = static_cast<int64_t>(RPS) * p.block_size * D * ES;
+        if (u.at < 0) rows = 0;  // no place: the rows are read and left
+    }
+    for (int i = 0; i < n; ++i, dst += way, rows -= RPS) {
+        // all but the newest kDepth - 2 copies have landed: this step's among them
+        asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
+        const uint4 raw0 = u.ring[u.slot * 64], raw1 = u.ring[u.slot * 64 + 32];
+        // the slot of the step before, whose row is used up, takes the next row
+        u.load.issue(p, u.ring + (u.slot == 0 ? kDepth - 1 : u.slot - 1) * 64, u.sub, u.c0, u.gap);
+        u.slot = u.slot == kDepth - 1 ? 0 : u.slot + 1;
+        const uint32_t x[8] = {raw0.x, raw0.y, raw0.z, raw0.w, raw1.x, raw1.y, raw1.z, raw1.w};
+        uint64_t y[8];
+        if constexpr (KIND != 2 || ES == 1) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = widen<DT>(x[e]);
+        }
+        if constexpr (KIND != 2) {
+            uint64_t r2 = 0;
+            if constexpr (NORM) {
+                uint64_t sa = mul2(y[0], y[0]), sb = mul2(y[4], y[4]);
+#pragma unroll
+                for (int e = 1; e < 4; ++e) {
+                    sa = fma2(y[e], y[e], sa);
+                    sb = fma2(y[4 + e], y[4 + e], sb);
+                }
+                const float2 s2 = unpair2(add2(sa, sb));
+                float ss = s2.x + s2.y;
+#pragma unroll
+                for (int d = 1; d < LPR; d <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+                float r = rsqrtf(fmaf(ss, 1.f / D, p.eps));
+                // squares past fp32's range (bf16 rows beyond 10^18): again on
+                // the row scaled by 2^-70, next to which eps is nothing
+                const bool big = !(ss < INFINITY);
+                if (__any_sync(0xffffffffu, big)) {
+                    const float down = big ? 8.470329472543003e-22f : 1.f;
+                    const uint64_t d2 = pair2(down, down);
+                    float sd = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        y[e] = mul2(y[e], d2);
+                        const float2 f = unpair2(y[e]);
+                        sd = fmaf(f.x, f.x, fmaf(f.y, f.y, sd));
+                    }
+#pragma unroll
+                    for (int d = 1; d < LPR; d <<= 1) sd += __shfl_xor_sync(0xffffffffu, sd, d);
+                    if (big) r = rsqrtf(sd * (1.f / D));
+                }
+                r2 = pair2(r, r);
+            }
+            // an element that nothing turns takes no part of another (which may be infinite)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                uint64_t z0, z1;  // the other elements of the pairs
+                if constexpr (INTER) {
+                    const float2 f = unpair2(y[e]), g = unpair2(y[4 + e]);
+                    z0 = pair2(f.y, f.x);
+                    z1 = pair2(g.y, g.x);
+                } else {
+                    z0 = y[4 + e];
+                    z1 = y[e];
+                }
+                y[e] = mul2(y[e], wc[e]);
+                y[4 + e] = mul2(y[4 + e], wc[4 + e]);
+                if (u.turned0) y[e] = fma2(z0, ws[e], y[e]);
+                if (u.turned1) y[4 + e] = fma2(z1, ws[4 + e], y[4 + e]);
+                if constexpr (NORM) {
+                    y[e] = mul2(y[e], r2);
+                    y[4 + e] = mul2(y[4 + e], r2);
+                }
+            }
+        }
+        if (rows <= 0) continue;
+        if constexpr (ES == 1) {
+            const float scale = KIND == 2 ? p.v_scale : p.k_scale;
+            *reinterpret_cast<uint2*>(dst) = e4m3_8(y, scale);
+            *reinterpret_cast<uint2*>(dst + u.gap) = e4m3_8(y + 4, scale);
+        } else {
+            // (elements that nothing changed keep their bits)
+            const bool vec = KIND == 0 ? p.qo_vec : KVT == kPacked ? p.ko_vec : true;
+            const bool new0 = KIND != 2 && (NORM || u.turned0), new1 = KIND != 2 && (NORM || u.turned1);
+            uint16_t* d16 = reinterpret_cast<uint16_t*>(dst);
+            store_row8(d16, new0 ? round_8<DT>(y) : raw0, vec);
+            store_row8(d16 + u.gap, new1 ? round_8<DT>(y + 4) : raw1, vec);
+        }
+    }
+}
+
+// DT: type of the rows; KVT: kPacked, DT (16-bit cache) or PA_FP8_E4M3
+template <int DT, int KVT, int D, bool INTER>
+__global__ void __launch_bounds__(kWarps * 32, kBlocks)
+qk_norm_rope_kernel(const NormRopeParams p) {
+    constexpr int LPR = D / 16;     // lanes per row, 16 elements each
+    constexpr int RPS = 32 / LPR;   // rows of a step
+    __shared__ __align__(16) float2 turn_all[kWarps][D / 2];
+    __shared__ uint4 ring_all[kWarps][kDepth][2][32];
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+    // this warp's run of steps, and the token and step it begins at
+    int64_t left = p.per_warp + (w < p.extra ? 1 : 0);
+    if (left == 0) return;
+    const int qs = (p.num_heads + RPS - 1) / RPS, ks = (p.num_kv_heads + RPS - 1) / RPS;
+    const int steps = qs + ks * (KVT == kPacked ? 1 : 2);
+    const int64_t begin = w * p.per_warp + (w < p.extra ? w : p.extra);
+    Run<KVT, D> u;
+    u.t = begin / steps;
+    int i = static_cast<int>(begin - u.t * steps);
+    int seg = i < qs ? 0 : i < qs + ks ? 1 : 2;
+    i -= seg == 0 ? 0 : seg == 1 ? qs : qs + ks;
+    u.ring = &ring_all[warp][0][0][lane];
+    u.slot = 0;
+    u.turn = turn_all[warp];
+    u.sub = lane / LPR;
+    u.half = p.rotary_dim / 16;
+    const int j = lane % LPR;
+    if (INTER) {
+        u.c0 = j;
+        u.gap = LPR * 8;
+        u.turned0 = j < 2 * u.half;
+        u.turned1 = j + LPR < 2 * u.half;
+    } else {
+        u.turned0 = u.turned1 = j < u.half;
+        u.c0 = j < u.half ? j : j + u.half;
+        u.gap = (j < u.half ? u.half : LPR - u.half) * 8;
+    }
+    u.at = -1;
+    u.next_pos = u.half > 0 ? __ldg(p.positions + u.t) : 0;
+    u.next_slot = KVT != kPacked ? __ldg(p.slots + u.t) : -1;
+    u.load.t = u.t;
+    u.load.seg = seg;
+    u.load.left = left;
+    u.load.enter(p, i, u.sub, u.c0);
+#pragma unroll
+    for (int k = 0; k < kDepth - 1; ++k) u.load.issue(p, u.ring + k * 64, u.sub, u.c0, u.gap);
+    enter_token(p, u);
+    while (left > 0) {
+        const int n = static_cast<int>(min(left, static_cast<int64_t>((seg == 0 ? qs : ks) - i)));
+        if (seg == 0) {
+            if (p.q_weight != nullptr) do_steps<DT, KVT, D, INTER, 0, true>(p, u, i, n);
+            else do_steps<DT, KVT, D, INTER, 0, false>(p, u, i, n);
+        } else if (seg == 1) {
+            if (p.k_weight != nullptr) do_steps<DT, KVT, D, INTER, 1, true>(p, u, i, n);
+            else do_steps<DT, KVT, D, INTER, 1, false>(p, u, i, n);
+        } else if constexpr (KVT != kPacked) {
+            do_steps<DT, KVT, D, INTER, 2, false>(p, u, i, n);
+        }
+        left -= n;
+        i = 0;
+        if (++seg == Loader<KVT, D>::kSegs && left > 0) {
+            seg = 0;
+            ++u.t;
+            enter_token(p, u);
+        }
+    }
+    // (the run's last groups are empty: no copy is on its way)
 }
 
 bool aligned16(const void* ptr, int64_t stride) {
     return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0 && stride % 8 == 0;
 }
 
-template <int DT, int KVT, int D>
+template <int DT, int KVT, int D, bool INTER>
 pa_status launch_t(NormRopeParams p, cudaStream_t stream) {
-    constexpr int RPS = 32 / (D / 8);
+    constexpr int RPS = 512 / D;
     const int64_t sms = device_sm_count();
     if (sms <= 0) return PA_ERR_CUDA;
     const int ks = (p.num_kv_heads + RPS - 1) / RPS;
     const int steps = (p.num_heads + RPS - 1) / RPS + ks * (KVT == kPacked ? 1 : 2);
-    // units of a token: one (its sines are worked out once), more while the
-    // units would not fill the SMs' warps a few times over
-    const int64_t want = sms * kUnitsPerSm / p.num_tokens;
-    const int64_t most = (steps + kMinSteps - 1) / kMinSteps;
-    const int parts = static_cast<int>(want < 1 ? 1 : (want < most ? want : most));
-    p.per_part = (steps + parts - 1) / parts;
-    p.parts = (steps + p.per_part - 1) / p.per_part;
-    const int64_t blocks = (p.num_tokens * p.parts + kWarps - 1) / kWarps;
-    if (blocks > INT32_MAX) return PA_ERR_UNSUPPORTED;
-    return launch_pdl(qk_norm_rope_kernel<DT, KVT, D>, static_cast<int>(blocks), kWarps * 32, 0, stream, p) ==
+    static LaunchCache cache;
+    const int per_sm = blocks_per_sm(qk_norm_rope_kernel<DT, KVT, D, INTER>, kWarps * 32, 0, cache);
+    if (per_sm <= 0) return PA_ERR_CUDA;
+    if (p.num_tokens > INT64_MAX / (1 << 20)) return PA_ERR_UNSUPPORTED;
+    const int64_t total = p.num_tokens * steps;
+    int64_t blocks = (total + kMinSteps * kWarps - 1) / (kMinSteps * kWarps);
+    if (blocks > sms * per_sm) blocks = sms * per_sm;
+    p.per_warp = total / (blocks * kWarps);
+    p.extra = total % (blocks * kWarps);
+    return launch_pdl(qk_norm_rope_kernel<DT, KVT, D, INTER>, static_cast<int>(blocks), kWarps * 32, 0, stream, p) ==
                    cudaSuccess
                ? PA_OK
                : PA_ERR_CUDA;
@@ -367,7 +510,8 @@ pa_status launch_t(NormRopeParams p, cudaStream_t stream) {
 
 pa_status launch(const NormRopeParams& p, int dt, int kvt, int head_size, cudaStream_t s) {
 #define PA_CASE(DT, KVT, D) \
-    if (dt == DT && kvt == KVT && head_size == D) return launch_t<DT, KVT, D>(p, s);
+    if (dt == DT && kvt == KVT && head_size == D)  \
+        return p.interleaved ? launch_t<DT, KVT, D, true>(p, s) : launch_t<DT, KVT, D, false>(p, s);
 #define PA_TYPES(D)                                                                              \
     PA_CASE(PA_F16, kPacked, D) PA_CASE(PA_F16, PA_F16, D) PA_CASE(PA_F16, PA_FP8_E4M3, D)       \
     PA_CASE(PA_BF16, kPacked, D) PA_CASE(PA_BF16, PA_BF16, D) PA_CASE(PA_BF16, PA_FP8_E4M3, D)
