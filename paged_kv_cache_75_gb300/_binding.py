@@ -277,42 +277,62 @@ class QKTransform:
             _need(self.rope.turns, "rope.turns", torch.int64)
 
     def c_struct(self, head_size: int, device) -> _QKTransform:
-        r = self.rope
-        for name, w in (("q_weight", self.q_weight), ("k_weight", self.k_weight)):
-            if w is not None and (w.dim() != 1 or w.shape[0] != head_size):
-                raise ValueError("%s must have head_size entries" % name)
-        for w in (self.q_weight, self.k_weight, None if r is None else r.turns):
-            if w is not None and w.device != device:
-                raise ValueError("the transform's tensors must be on the rows' device")
-        return _QKTransform(_addr(self.q_weight), _addr(self.k_weight), float(self.eps),
-                            None if r is None else r.turns.data_ptr(), 1.0 if r is None else float(r.factor),
-                            0 if r is None else r.rotary_dim, 1 if self.interleaved else 0)
+        r, qw, kw = self.rope, self.q_weight, self.k_weight
+        c = _QKTransform(eps=self.eps, rope_factor=1.0, interleaved=1 if self.interleaved else 0)
+        if qw is not None:
+            c.q_weight = _on_device(qw, "q_weight", head_size, device)
+        if kw is not None:
+            c.k_weight = _on_device(kw, "k_weight", head_size, device)
+        if r is not None:
+            n = r.turns.shape[0]
+            c.turns = _on_device(r.turns, "rope.turns", n, device)
+            c.rope_factor = r.factor
+            c.rotary_dim = 2 * n
+        return c
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
+def _on_device(t, name, n, device):
+    if t.shape != (n,) or t.device != device:
+        raise ValueError("%s must have %d entries on the rows' device" % (name, n))
+    return t.data_ptr()
 
 
-def _rows(t, name, tokens=None, heads=None, head_size=None, like=None):
-    """Checks [T, heads, head_size] rows whose tokens may be strided."""
+def _rows(t, name, shape, dtype, device):
+    """Checks [T, heads, head_size] rows whose tokens may be strided; returns
+    the token stride."""
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        raise ValueError("%s must be %s %s on %s" % (name, dtype, tuple(shape), device))
+    T, n, D = shape
+    st, sh, sd = t.stride()
+    if sd != 1 or (sh != D and n > 1):
+        raise ValueError("the heads of a token of %s must be contiguous" % name)
+    return st if T > 1 else max(st, n * D)  # (a single token's stride says nothing)
+
+
+def _rows_of(t, name):
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3:
         raise ValueError("%s must be a CUDA tensor [tokens, heads, head_size]" % name)
-    T, n, D = t.shape
-    if (tokens is not None and T != tokens) or (heads is not None and n != heads) or \
-            (head_size is not None and D != head_size):
-        raise ValueError("%s has the wrong shape %s" % (name, tuple(t.shape)))
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
-        raise ValueError("%s must have the queries' type and device" % name)
-    if (D > 1 and t.stride(2) != 1) or (n > 1 and t.stride(1) != D):
-        raise ValueError("the heads of a token of %s must be contiguous" % name)
-    # (a single token's stride says nothing)
-    return max(t.stride(0), n * D) if T <= 1 else t.stride(0)
+    return t.shape
 
 
 def _token_index(t, name, tokens, device):
-    _need(t, name, torch.int64)
-    if t.dim() != 1 or t.shape[0] != tokens or t.device != device:
-        raise ValueError("%s must be int64 [tokens] on the queries' device" % name)
+    if t.dtype != torch.int64:
+        raise TypeError("%s must be torch.int64" % name)
+    if t.shape != (tokens,) or t.device != device or not t.is_contiguous():
+        raise ValueError("%s must be contiguous int64 [tokens] on the queries' device" % name)
+    return t.data_ptr()
+
+
+def _status_ptr(t, device):
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.device != device:
+        raise ValueError("dev_status must be int32 on the queries' device")
+    return t.data_ptr()
+
+
+def _raw_stream(device):
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def pa_qk_norm_rope(q_out: torch.Tensor, k_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
@@ -321,16 +341,19 @@ def pa_qk_norm_rope(q_out: torch.Tensor, k_out: torch.Tensor, q: torch.Tensor, k
     num_kv_heads, head_size] (tokens may be strided: views of a fused qkv buffer)
     into q_out and k_out of the same shapes, which may be q and k themselves;
     positions: int64 [T]."""
-    qs = _rows(q, "q")
-    T, H, D = q.shape
-    ks = _rows(k, "k", T, None, D, q)
-    qos, kos = _rows(q_out, "q_out", T, H, D, q), _rows(k_out, "k_out", T, k.shape[1], D, q)
-    if positions is not None:
-        _token_index(positions, "positions", T, q.device)
-    tr = transform.c_struct(D, q.device)
-    with _on(q.device):
-        st = library().pa_qk_norm_rope(_ptr(q_out), _ptr(k_out), _ptr(q), _ptr(k), torch_dtype_code(q.dtype), T, H,
-                                       k.shape[1], D, qs, ks, qos, kos, _ptr(positions), C.byref(tr), _stream(q))
+    shape, kshape = _rows_of(q, "q"), _rows_of(k, "k")
+    T, H, D = shape
+    dt, dev = q.dtype, q.device
+    if kshape[0] != T or kshape[2] != D:
+        raise ValueError("k must have the queries' tokens and head size")
+    qs, ks = _rows(q, "q", shape, dt, dev), _rows(k, "k", kshape, dt, dev)
+    qos, kos = _rows(q_out, "q_out", shape, dt, dev), _rows(k_out, "k_out", kshape, dt, dev)
+    pos = None if positions is None else _token_index(positions, "positions", T, dev)
+    tr = transform.c_struct(D, dev)
+    with _on(dev):
+        st = library().pa_qk_norm_rope(q_out.data_ptr(), k_out.data_ptr(), q.data_ptr(), k.data_ptr(),
+                                       torch_dtype_code(dt), T, H, kshape[1], D, qs, ks, qos, kos, pos, tr,
+                                       _raw_stream(dev))
     _check(st, "pa_qk_norm_rope")
 
 
@@ -339,21 +362,22 @@ def pa_qk_norm_rope_write(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
                           dev_status: Optional[torch.Tensor] = None):
     """pa_qk_norm_rope with the keys, and the values v as they are, written to
     slot_mapping's (int64 [T], < 0 skips) slots of the cache."""
-    qs = _rows(q, "q")
-    T, H, D = q.shape
-    Hkv = cache.num_kv_heads
-    if D != cache.head_size or cache.k_cache.device != q.device:
+    shape = _rows_of(q, "q")
+    T, H, D = shape
+    dt, dev = q.dtype, q.device
+    cs = cache.c_struct()
+    if D != cs.head_size or cache.k_cache.device != dev:
         raise ValueError("the cache must have the queries' head size and device")
-    ks, vs = _rows(k, "k", T, Hkv, D, q), _rows(v, "v", T, Hkv, D, q)
-    qos = _rows(q_out, "q_out", T, H, D, q)
-    if positions is not None:
-        _token_index(positions, "positions", T, q.device)
-    _token_index(slot_mapping, "slot_mapping", T, q.device)
-    cs, tr = cache.c_struct(), transform.c_struct(D, q.device)
-    with _on(q.device):
-        st = library().pa_qk_norm_rope_write(_ptr(q_out), _ptr(q), _ptr(k), _ptr(v), torch_dtype_code(q.dtype),
-                                             C.byref(cs), T, H, qs, ks, vs, qos, _ptr(positions), _ptr(slot_mapping),
-                                             C.byref(tr), _ptr(dev_status), _stream(q))
+    kshape = (T, cs.num_kv_heads, D)
+    qs, ks, vs = _rows(q, "q", shape, dt, dev), _rows(k, "k", kshape, dt, dev), _rows(v, "v", kshape, dt, dev)
+    qos = _rows(q_out, "q_out", shape, dt, dev)
+    pos = None if positions is None else _token_index(positions, "positions", T, dev)
+    slots = _token_index(slot_mapping, "slot_mapping", T, dev)
+    tr = transform.c_struct(D, dev)
+    with _on(dev):
+        st = library().pa_qk_norm_rope_write(q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                             torch_dtype_code(dt), cs, T, H, qs, ks, vs, qos, pos, slots, tr,
+                                             _status_ptr(dev_status, dev), _raw_stream(dev))
     _check(st, "pa_qk_norm_rope_write")
 
 

@@ -25,8 +25,9 @@
 // rotary_dim/16 in the half layout (the lanes past the rotated part share the
 // rest), whole pairs in any chunk when interleaved.  No element changes lanes,
 // the sum of squares is all that does.  A warp takes a step of 4 heads (8 of
-// 64 elements) at a time.  The call's steps (all tokens' queries, keys, values)
-// are dealt out to the resident warps in equal contiguous runs.  Each lane keeps
+// 64 elements) at a time.  The resident warps take a token each, round by
+// round, and the last round's steps (what its tokens have of queries, keys and
+// values) are dealt out in equal runs.  Each lane keeps
 // the next rows in flight through a ring of its own in shared memory (16-byte
 // asynchronous copies that only the same lane reads back: no barrier, and no
 // register held while a load is on its way).  When a run enters a token, the warp
@@ -43,8 +44,8 @@ namespace pa {
 namespace {
 
 constexpr int kWarps = 4;     // warps of a block
-constexpr int kBlocks = 5;    // blocks per SM that the registers allow
-constexpr int kDepth = 8;     // steps a lane's ring holds
+constexpr int kBlocks = 4;    // blocks per SM that the registers allow
+constexpr int kDepth = 4;     // steps a lane's ring holds
 constexpr int kMinSteps = 1;  // steps of a warp's run, at least
 constexpr int kPacked = -1;   // keys go to packed rows, there is no cache
 
@@ -67,7 +68,9 @@ struct NormRopeParams {
     float eps, rope_factor, k_scale, v_scale;
     int32_t num_heads, num_kv_heads;
     int32_t rotary_dim, interleaved, block_size;
-    int64_t per_warp, extra;  // steps of a warp's run: per_warp, one more for the first `extra` warps
+    // each warp takes tokens w, w + warps, ... for `rounds` rounds, then a run of
+    // the remaining tokens' steps: per_warp, one more for the first `extra` warps
+    int64_t warps, rounds, per_warp, extra;
     // 16-byte accesses allowed (pointer and stride aligned)
     bool q_vec, k_vec, v_vec, qo_vec, ko_vec;
 };
@@ -158,21 +161,36 @@ __device__ __forceinline__ uint4 round_8(const uint64_t* x) {
     return make_uint4(y[0], y[1], y[2], y[3]);
 }
 
-// The rows that a warp's run loads: a cursor over (token, segment, step), the
+// A warp's tokens in turn: one a round, then those of its last run.
+struct Tokens {
+    int64_t t, round, last;  // last: the last run's first token
+    __device__ __forceinline__ int64_t after(const NormRopeParams& p) const {
+        return round + 1 < p.rounds ? t + p.warps : round + 1 == p.rounds ? last : t + 1;
+    }
+    __device__ __forceinline__ void next(const NormRopeParams& p) {
+        t = after(p);
+        ++round;
+    }
+};
+
+// The rows that a warp loads: a cursor over (token, segment, step), the
 // segments of a token being its queries (0), keys (1) and values (2).
 template <int KVT, int D>
 struct Loader {
     static constexpr int RPS = 512 / D;  // rows of a step
     static constexpr int kSegs = KVT == kPacked ? 2 : 3;
     const uint16_t* src;  // this lane's first chunk of the step's row
-    int64_t t;
-    int64_t left;  // steps of the run not yet issued
+    Tokens at;
+    int64_t left;  // steps not yet issued
+    int first_seg, first_step;  // where the last run begins in its token
     int rows;      // rows of the segment from this lane's on
     int seg;
     bool vec;
 
     __device__ __forceinline__ void enter(const NormRopeParams& p, int step, int sub, int c0) {
-        const uint16_t* base = seg == 0 ? p.q + t * p.q_stride : seg == 1 ? p.k + t * p.k_stride : p.v + t * p.v_stride;
+        const uint16_t* base = seg == 0   ? p.q + at.t * p.q_stride
+                               : seg == 1 ? p.k + at.t * p.k_stride
+                                          : p.v + at.t * p.v_stride;
         vec = seg == 0 ? p.q_vec : seg == 1 ? p.k_vec : p.v_vec;
         rows = (seg == 0 ? p.num_heads : p.num_kv_heads) - step * RPS - sub;
         src = base + (step * RPS + sub) * D + c0 * 8;
@@ -200,11 +218,16 @@ struct Loader {
             rows -= RPS;
             // (the segment's last step: no row is left for the step's first lanes)
             if (rows + sub <= 0 && left > 0) {
+                int step = 0;
                 if (++seg == kSegs) {
                     seg = 0;
-                    ++t;
+                    at.next(p);
+                    if (at.round == p.rounds) {
+                        seg = first_seg;
+                        step = first_step;
+                    }
                 }
-                enter(p, 0, sub, c0);
+                enter(p, step, sub, c0);
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -218,7 +241,7 @@ struct Run {
     Loader<KVT, D> load;
     uint4* ring;      // [kDepth][2][32], this lane's slots
     int slot;         // of the step to work on
-    int64_t t;
+    Tokens tok;
     int64_t at;       // cache row of the token's KV head 0, -1 for none
     float2* turn;     // shared memory: (cos, sin) * factor of the token's pairs
     int64_t pos, next_pos;
@@ -253,9 +276,10 @@ __device__ __forceinline__ void enter_token(const NormRopeParams& p, Run<KVT, D>
     u.ready = false;
     u.pos = u.next_pos;
     const int64_t slot = u.next_slot;
-    if (u.t + 1 < p.num_tokens) {
-        if (u.half > 0) u.next_pos = __ldg(p.positions + u.t + 1);
-        if (KVT != kPacked) u.next_slot = __ldg(p.slots + u.t + 1);
+    const int64_t after = u.tok.after(p);
+    if (after < p.num_tokens) {
+        if (u.half > 0) u.next_pos = __ldg(p.positions + after);
+        if (KVT != kPacked) u.next_slot = __ldg(p.slots + after);
     }
     if (KVT != kPacked) {
         u.at = -1;
@@ -317,10 +341,10 @@ __device__ __forceinline__ void do_steps(const NormRopeParams& p, Run<KVT, D>& u
     int rows = (KIND == 0 ? p.num_heads : p.num_kv_heads) - s0 * RPS - u.sub;
     const int64_t h0 = s0 * RPS + u.sub;
     if constexpr (KIND == 0) {
-        dst = reinterpret_cast<uint8_t*>(p.q_out + u.t * p.qo_stride + h0 * D + u.c0 * 8);
+        dst = reinterpret_cast<uint8_t*>(p.q_out + u.tok.t * p.qo_stride + h0 * D + u.c0 * 8);
         way = RPS * D * 2;
     } else if constexpr (KVT == kPacked) {
-        dst = reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(p.k_out) + u.t * p.ko_stride + h0 * D + u.c0 * 8);
+        dst = reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(p.k_out) + u.tok.t * p.ko_stride + h0 * D + u.c0 * 8);
         way = RPS * D * 2;
     } else {
         dst = static_cast<uint8_t*>(KIND == 2 ? p.v_out : p.k_out) + ((u.at + h0 * p.block_size) * D + u.c0 * 8) * ES;
@@ -423,17 +447,22 @@ qk_norm_rope_kernel(const NormRopeParams p) {
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
-    // this warp's run of steps, and the token and step it begins at
-    int64_t left = p.per_warp + (w < p.extra ? 1 : 0);
-    if (left == 0) return;
     const int qs = (p.num_heads + RPS - 1) / RPS, ks = (p.num_kv_heads + RPS - 1) / RPS;
     const int steps = qs + ks * (KVT == kPacked ? 1 : 2);
+    // the last run: the token, segment and step it begins at
     const int64_t begin = w * p.per_warp + (w < p.extra ? w : p.extra);
+    const int64_t run = p.per_warp + (w < p.extra ? 1 : 0);
+    int64_t left = p.rounds * steps + run;
+    if (left == 0) return;
     Run<KVT, D> u;
-    u.t = begin / steps;
-    int i = static_cast<int>(begin - u.t * steps);
-    int seg = i < qs ? 0 : i < qs + ks ? 1 : 2;
-    i -= seg == 0 ? 0 : seg == 1 ? qs : qs + ks;
+    u.tok.last = p.rounds * p.warps + begin / steps;
+    int i = static_cast<int>(begin % steps);
+    u.load.first_seg = i < qs ? 0 : i < qs + ks ? 1 : 2;
+    u.load.first_step = i - (i < qs ? 0 : i < qs + ks ? qs : qs + ks);
+    u.tok.round = 0;
+    u.tok.t = p.rounds > 0 ? w : u.tok.last;
+    int seg = p.rounds > 0 ? 0 : u.load.first_seg;
+    i = p.rounds > 0 ? 0 : u.load.first_step;
     u.ring = &ring_all[warp][0][0][lane];
     u.slot = 0;
     u.turn = turn_all[warp];
@@ -451,9 +480,9 @@ qk_norm_rope_kernel(const NormRopeParams p) {
         u.gap = (j < u.half ? u.half : LPR - u.half) * 8;
     }
     u.at = -1;
-    u.next_pos = u.half > 0 ? __ldg(p.positions + u.t) : 0;
-    u.next_slot = KVT != kPacked ? __ldg(p.slots + u.t) : -1;
-    u.load.t = u.t;
+    u.next_pos = u.half > 0 ? __ldg(p.positions + u.tok.t) : 0;
+    u.next_slot = KVT != kPacked ? __ldg(p.slots + u.tok.t) : -1;
+    u.load.at = u.tok;
     u.load.seg = seg;
     u.load.left = left;
     u.load.enter(p, i, u.sub, u.c0);
@@ -475,7 +504,11 @@ qk_norm_rope_kernel(const NormRopeParams p) {
         i = 0;
         if (++seg == Loader<KVT, D>::kSegs && left > 0) {
             seg = 0;
-            ++u.t;
+            u.tok.next(p);
+            if (u.tok.round == p.rounds) {
+                seg = u.load.first_seg;
+                i = u.load.first_step;
+            }
             enter_token(p, u);
         }
     }
@@ -500,8 +533,11 @@ pa_status launch_t(NormRopeParams p, cudaStream_t stream) {
     const int64_t total = p.num_tokens * steps;
     int64_t blocks = (total + kMinSteps * kWarps - 1) / (kMinSteps * kWarps);
     if (blocks > sms * per_sm) blocks = sms * per_sm;
-    p.per_warp = total / (blocks * kWarps);
-    p.extra = total % (blocks * kWarps);
+    p.warps = blocks * kWarps;
+    p.rounds = p.num_tokens / p.warps;
+    const int64_t rest = total - p.rounds * p.warps * steps;
+    p.per_warp = rest / p.warps;
+    p.extra = rest % p.warps;
     return launch_pdl(qk_norm_rope_kernel<DT, KVT, D, INTER>, static_cast<int>(blocks), kWarps * 32, 0, stream, p) ==
                    cudaSuccess
                ? PA_OK
