@@ -301,6 +301,32 @@ pa_status pa_decode_static_ws(void* out, const void* q, pa_dtype q_dtype, const 
                               int32_t* dev_status, pa_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Single-query decode with a sliding window and sinks.  (The pages attend the
+ * whole context; this is the mask of layers whose queries see only the last
+ * tokens and, so that the softmax keeps its anchor, a few first ones.)
+ *
+ * As pa_decode, but the query of sequence b, at position L - 1 (L = seq_lens[b]),
+ * sees the positions t < L with
+ *     t >= L - window   or   t < num_sinks,
+ * window >= 1 counting the query's own position, num_sinks >= 0.  A window or a
+ * sink count of L or more gives pa_decode's result.  Only the blocks that hold a
+ * visible position are read: a row's other entries may be anything (-1 after
+ * pa_pool_release_window), and what the blocks hold at positions that are not
+ * seen (NaN included) takes no part.
+ * partition_size counts the tokens of the blocks read (the sinks' whole blocks,
+ * then the window's); 0 chooses one.  workspace: pa_decode_window_workspace_size
+ * (...) bytes with the same arguments.  Everything else as pa_decode.
+ * ------------------------------------------------------------------------- */
+size_t pa_decode_window_workspace_size(int32_t num_seqs, int32_t num_heads, int32_t head_size, int32_t max_seq_len,
+                                       int32_t block_size, int32_t window, int32_t num_sinks,
+                                       int32_t partition_size);
+pa_status pa_decode_window(void* out, const void* q, pa_dtype q_dtype, const pa_kv_cache* cache,
+                           const int32_t* block_table, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                           int32_t num_seqs, int32_t max_seq_len, int32_t num_heads, float scale, int32_t window,
+                           int32_t num_sinks, int32_t partition_size, void* workspace, size_t workspace_bytes,
+                           int32_t* dev_status, pa_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Varlen prefill (and mixed prefill + decode) attention over the paged cache.
  * "Paged 어텐션" Varlen 경로 (cu_seq_lens_q/k index a batch of sequences of
  * different lengths; max_seqlen_q/k bound them); keys and values are read

@@ -59,6 +59,9 @@ def library():
             "pa_decode_workspace_size": ([i32, i32, i32, i32, i32, i32], sz),
             "pa_decode": ([vp, vp, C.c_int, pc, vp, i32, vp, i32, i32, i32, f32, i32, vp, sz, vp, vp],
                           C.c_int),
+            "pa_decode_window_workspace_size": ([i32, i32, i32, i32, i32, i32, i32, i32], sz),
+            "pa_decode_window": ([vp, vp, C.c_int, pc, vp, i32, vp, i32, i32, i32, f32, i32, i32, i32, vp, sz, vp, vp],
+                                 C.c_int),
             "pa_prefill_varlen": ([vp, vp, C.c_int, pc, vp, i32, vp, vp, i32, i32, i32, i32, f32, i32,
                                    vp, vp], C.c_int),
             "pa_pool_create": ([i64, i32, vp, C.POINTER(vp)], C.c_int),
@@ -480,6 +483,48 @@ def pa_decode(out: torch.Tensor, q: torch.Tensor, cache: KVCache, block_table: t
                              block_table.shape[1], _ptr(seq_lens), B, int(max_seq_len), H, float(scale),
                              int(partition_size), _ptr(workspace), ws_bytes, _ptr(dev_status), _stream(q))
     _check(st, "pa_decode")
+
+
+def pa_decode_window_workspace_size(num_seqs, num_heads, head_size, max_seq_len, block_size, window, num_sinks=0,
+                                    partition_size=0) -> int:
+    return int(library().pa_decode_window_workspace_size(num_seqs, num_heads, head_size, max_seq_len, block_size,
+                                                         window, num_sinks, partition_size))
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError("%s must be on the queries' device" % name)
+
+
+def pa_decode_window(out: torch.Tensor, q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
+                     seq_lens: torch.Tensor, max_seq_len: int, scale: float, window: int, num_sinks: int = 0,
+                     partition_size: int = 0, workspace: Optional[torch.Tensor] = None,
+                     dev_status: Optional[torch.Tensor] = None):
+    """pa_decode where each query sees the last `window` tokens (its own
+    included) and the first num_sinks; block-table entries of blocks that hold
+    neither are not read."""
+    _need(q, "q")
+    _need(out, "out", q.dtype)
+    _need(block_table, "block_table", torch.int32)
+    _need(seq_lens, "seq_lens", torch.int32)
+    B, H, D = q.shape
+    dev = q.device
+    if out.shape != q.shape or block_table.dim() != 2 or block_table.shape[0] != B or seq_lens.shape != (B,) or \
+            D != cache.head_size:
+        raise ValueError("out must have q's shape, block_table [num_seqs, max_blocks], seq_lens [num_seqs], the cache "
+                         "q's head size")
+    _same_device(dev, out=out, cache=cache.k_cache, block_table=block_table, seq_lens=seq_lens, workspace=workspace)
+    if workspace is not None:
+        _need(workspace, "workspace")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    with _on(dev):
+        st = library().pa_decode_window(out.data_ptr(), q.data_ptr(), torch_dtype_code(q.dtype), cache.c_struct(),
+                                        block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), B,
+                                        int(max_seq_len), H, float(scale), int(window), int(num_sinks),
+                                        int(partition_size), None if workspace is None else workspace.data_ptr(),
+                                        ws_bytes, _status_ptr(dev_status, dev), _raw_stream(dev))
+    _check(st, "pa_decode_window")
 
 
 def pa_decode_test_wait_timeout(out: torch.Tensor, q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,

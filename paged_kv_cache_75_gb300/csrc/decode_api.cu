@@ -50,6 +50,25 @@ struct WsLayout {
     size_t lse_off, o_off, bytes;
 };
 
+// Windowed decode: the most tokens a sequence's visible blocks hold.  The sinks'
+// ceil(sinks / bs) blocks, the window's tokens and the rest of the window's first
+// block (window_span: L - skip * bs).
+int window_tokens(int max_seq_len, int block_size, int window, int sinks) {
+    const int64_t n = (static_cast<int64_t>(sinks) + block_size - 1) / block_size * block_size + window + block_size - 1;
+    return static_cast<int>(n < max_seq_len ? n : max_seq_len);
+}
+
+// Windowed decode, automatic partition: the plain choice for those tokens, cut
+// into equal parts (most sequences are longer than the window, so their parts
+// are alike, where 1536 tokens of 2100 would leave a third of the blocks a part
+// of 564).
+int window_partition(int64_t num_seqs, int num_kv_heads, int tokens, int group, int block_size) {
+    const int p = auto_partition(num_seqs, num_kv_heads, tokens, group);
+    const int n = (tokens + p - 1) / p;
+    if (n <= 1) return p;
+    return ((tokens + n - 1) / n + block_size - 1) / block_size * block_size;
+}
+
 WsLayout ws_layout(int64_t num_seqs, int64_t num_heads, int64_t head_size, int max_parts) {
     WsLayout w{0, 0, 0};
     if (max_parts <= 1) return w;
@@ -86,7 +105,7 @@ pa_status decode_entry(void* out, const void* q, pa_dtype q_dtype, const pa_kv_c
                        pa_stream_t stream, const void* k_new, const void* v_new,
                        const int32_t* cu_seq_lens_k = nullptr, const int32_t* cu_groups = nullptr,
                        const int32_t* shared_lens = nullptr, int32_t num_groups = 0, bool group_mode = false,
-                       int32_t max_group_size = 0, bool no_copies = false) {
+                       int32_t max_group_size = 0, bool no_copies = false, int32_t window = 0, int32_t sinks = 0) {
     pa_status st = check_cache(cache);
     if (st != PA_OK) return st;
     if (num_seqs < 0 || num_heads <= 0 || max_blocks_per_seq <= 0 || max_seq_len < 0 ||
@@ -113,7 +132,11 @@ pa_status decode_entry(void* out, const void* q, pa_dtype q_dtype, const pa_kv_c
         !(cache->k_scale > 0.f && std::isfinite(cache->k_scale) && cache->v_scale > 0.f &&
           std::isfinite(cache->v_scale)))
         return PA_ERR_INVALID_ARG;
-    const int P = resolve_partition(partition_size, num_seqs, cache->num_kv_heads, max_seq_len, group);
+    // (windowed: the partitions are of the visible blocks' tokens)
+    const int max_tokens = window > 0 ? window_tokens(max_seq_len, bs, window, sinks) : max_seq_len;
+    const int P = window > 0 && partition_size == 0
+                      ? window_partition(num_seqs, cache->num_kv_heads, max_tokens, group, bs)
+                      : resolve_partition(partition_size, num_seqs, cache->num_kv_heads, max_tokens, group);
     if (P % bs != 0) return PA_ERR_INVALID_ARG;
     if (num_seqs > 16384) return PA_ERR_UNSUPPORTED;
     if (cu_groups != nullptr && (shared_lens == nullptr || num_groups <= 0 || k_new != nullptr))
@@ -127,7 +150,7 @@ pa_status decode_entry(void* out, const void* q, pa_dtype q_dtype, const pa_kv_c
     if (group_mode && num_groups * vpg + num_seqs > 16384) return PA_ERR_UNSUPPORTED;
     // cascade: the prefix's parts (ceil(s0/P)) and the suffix's (parts_of(L-s0))
     // never exceed parts_of(L) + 1
-    const int max_parts = max_parts_of(max_seq_len, P) + (cu_groups != nullptr ? 1 : 0);
+    const int max_parts = max_parts_of(max_tokens, P) + (cu_groups != nullptr ? 1 : 0);
     const WsLayout w = ws_layout(num_seqs, num_heads, D, max_parts);
     if (w.bytes > 0 && (workspace == nullptr || workspace_bytes < w.bytes ||
                         (reinterpret_cast<uintptr_t>(workspace) & 15u)))
@@ -165,6 +188,8 @@ pa_status decode_entry(void* out, const void* q, pa_dtype q_dtype, const pa_kv_c
     p.num_groups = num_groups;
     p.num_members = num_seqs;
     p.no_copies = no_copies ? 1 : 0;
+    p.window = window;
+    p.sinks = sinks;
     int kgroup = group;
     if (group_mode) {
         p.vm = vm;
@@ -197,6 +222,31 @@ extern "C" pa_status pa_decode(void* out, const void* q, pa_dtype q_dtype, const
     return pa::decode_entry(out, q, q_dtype, cache, block_table, max_blocks_per_seq, seq_lens, num_seqs,
                             max_seq_len, num_heads, scale, partition_size, workspace, workspace_bytes, dev_status,
                             stream, nullptr, nullptr);
+}
+
+extern "C" size_t pa_decode_window_workspace_size(int32_t num_seqs, int32_t num_heads, int32_t head_size,
+                                                  int32_t max_seq_len, int32_t block_size, int32_t window,
+                                                  int32_t num_sinks, int32_t partition_size) {
+    if (num_seqs <= 0 || num_heads <= 0 || head_size <= 0 || max_seq_len < 0 || block_size <= 0 || window <= 0 ||
+        num_sinks < 0 || partition_size < 0)
+        return 0;
+    const int tokens = window_tokens(max_seq_len, block_size, window, num_sinks);
+    // an automatic choice never has more parts than partitions of 512: equal parts
+    // keep the count of the plain choice
+    return ws_layout(num_seqs, num_heads, head_size, max_parts_of(tokens, ws_partition(partition_size))).bytes;
+}
+
+extern "C" pa_status pa_decode_window(void* out, const void* q, pa_dtype q_dtype, const pa_kv_cache* cache,
+                                      const int32_t* block_table, int32_t max_blocks_per_seq,
+                                      const int32_t* seq_lens, int32_t num_seqs, int32_t max_seq_len,
+                                      int32_t num_heads, float scale, int32_t window, int32_t num_sinks,
+                                      int32_t partition_size, void* workspace, size_t workspace_bytes,
+                                      int32_t* dev_status, pa_stream_t stream) {
+    if (window <= 0 || num_sinks < 0) return PA_ERR_INVALID_ARG;
+    return pa::decode_entry(out, q, q_dtype, cache, block_table, max_blocks_per_seq, seq_lens, num_seqs,
+                            max_seq_len, num_heads, scale, partition_size, workspace, workspace_bytes, dev_status,
+                            stream, nullptr, nullptr, nullptr, nullptr, nullptr, 0, false, 0, false, window,
+                            num_sinks);
 }
 
 extern "C" pa_status pa_decode_append(void* out, const void* q, const void* k_new, const void* v_new,

@@ -91,11 +91,19 @@ struct DecodeParams {
     int32_t vcount;
     int32_t g_real;
     int32_t num_members;
+    // windowed decode (pa_decode_window): a query sees the last `window` tokens
+    // and the first `sinks`
+    int32_t window;
+    int32_t sinks;
     // test hook (pa_decode_test_wait_timeout; 0 on every other path): the
     // producer warp issues no copy at all, so every consumer wait runs out
     // with nothing in flight, reports PA_ERR_TIMEOUT and the block returns
     int32_t no_copies;
 };
+
+// What a launch does besides attending: nothing, write the new token first
+// (pa_decode_append), or attend a window and sinks (pa_decode_window).
+enum DecodeMode { kPlain = 0, kAppend = 1, kWindow = 2 };
 
 template <int QDT, int KVDT, int D, int G, int BS>
 struct DecodeCfg {
@@ -196,6 +204,26 @@ __device__ __forceinline__ int group_of(const DecodeParams& p, int b) {
     return lo;
 }
 
+// Windowed decode: what sequence b of length L reads.  Of its blocks, those that
+// hold a visible token are the first `head` (the sinks') and, skipping `skip`
+// blocks, the rest from the window's first one on.  The kernel works on these
+// alone, as if they were the whole sequence: "length" L - skip * block_size,
+// position v standing for v (+ skip * block_size past the sinks' blocks).  There,
+// v is visible if v < sinks or v >= lo (skip > 0: the sinks' last block ends at or
+// before lo, so both tests are one rule).
+struct WindowSpan {
+    int sinks, lo, head, skip;
+};
+__device__ __forceinline__ WindowSpan window_span(const DecodeParams& p, int L) {
+    WindowSpan w;
+    w.sinks = min(p.sinks, L);
+    const int lo = L > p.window ? L - p.window : 0;
+    w.head = (w.sinks + p.block_size - 1) / p.block_size;
+    w.skip = max(0, lo / p.block_size - w.head);
+    w.lo = lo - w.skip * p.block_size;
+    return w;
+}
+
 // Group mode: the members sequence b stands for (m0 .. m0+nm-1; nm = 0 past
 // a group's end or for a malformed cu_groups) and whether it is a member's own
 // tokens (b >= vcount) rather than its group's shared ones.
@@ -237,7 +265,7 @@ __device__ __forceinline__ int seq_start(const DecodeParams& p, int b, int L) {
 }
 
 // A length is usable iff 0 <= L <= max_seq_len and L fits the table row.
-__device__ __forceinline__ int checked_len(const DecodeParams& p, int b) {
+__device__ __forceinline__ int true_len(const DecodeParams& p, int b) {
     if (p.vm > 0 && b >= p.vcount) b -= p.vcount;  // group mode: a member's own tokens
     else if (p.vm > 0) {
         // group mode: the group's shared blocks, for a sequence with members
@@ -254,6 +282,15 @@ __device__ __forceinline__ int checked_len(const DecodeParams& p, int b) {
                                        : __ldg(p.seq_lens + b);
     if (L < 0 || L > p.max_seq_len || static_cast<int64_t>(L) > static_cast<int64_t>(p.max_blocks) * p.block_size)
         return -1;
+    return L;
+}
+
+// The tokens a launch works on: the length, or (WIN) what is left of it without
+// the blocks between the sinks and the window.
+template <bool WIN>
+__device__ __forceinline__ int checked_len(const DecodeParams& p, int b) {
+    const int L = true_len(p, b);
+    if constexpr (WIN) return L <= 0 ? L : L - window_span(p, L).skip * p.block_size;
     return L;
 }
 
@@ -276,6 +313,7 @@ __device__ __forceinline__ int tail_class(int L, int P) {
     return static_cast<int>((static_cast<int64_t>(P - t) * 64) / (P + 1));  // 0 = longest
 }
 
+template <bool WIN>
 __device__ inline void build_schedule(const DecodeParams& p, int32_t* prefix, int32_t* order, int32_t* scratch,
                                       uint8_t* keys, int32_t* hist) {
     const int B = p.num_seqs;
@@ -284,7 +322,7 @@ __device__ inline void build_schedule(const DecodeParams& p, int32_t* prefix, in
     const int b0 = t * chunk, b1 = min(B, b0 + chunk);
     int local = 0;
     for (int b = b0; b < b1; ++b) {
-        int L = checked_len(p, b);
+        int L = checked_len<WIN>(p, b);
         if (L < 0) report(p.status, PA_ERR_INVALID_ARG);
         L = L < 0 ? 0 : L;
         const int n = L - seq_start(p, b, L);
@@ -314,7 +352,7 @@ __device__ inline void build_schedule(const DecodeParams& p, int32_t* prefix, in
     int run = scratch[warp] + v - local;
     for (int b = b0; b < b1; ++b) {
         prefix[b] = run;
-        int L = checked_len(p, b);
+        int L = checked_len<WIN>(p, b);
         L = L < 0 ? 0 : L;
         run += parts_of(L - seq_start(p, b, L), p.partition) - 1;
     }
@@ -373,8 +411,10 @@ __device__ inline void build_schedule(const DecodeParams& p, int32_t* prefix, in
 
 struct Item {
     int b, part, kvh, L, s0, t1, j0, j1, nparts;
+    int sinks, lo, head, skip;  // windowed decode: WindowSpan (all positions without the skipped blocks)
 };
 
+template <bool WIN>
 __device__ __forceinline__ Item decode_item(const DecodeParams& p, const int32_t* prefix, const int32_t* order,
                                             int i) {
     Item it;
@@ -391,23 +431,43 @@ __device__ __forceinline__ Item decode_item(const DecodeParams& p, const int32_t
         }
         it.b = lo;
         it.part = sp - prefix[lo];
-        L = checked_len(p, lo);
+        L = checked_len<WIN>(p, lo);
         it.L = L < 0 ? 0 : L;
         it.s0 = seq_start(p, lo, it.L);
         it.nparts = parts_of(it.L - it.s0, p.partition);
     } else {
         it.b = order[sp - F];
-        L = checked_len(p, it.b);
+        L = checked_len<WIN>(p, it.b);
         it.L = L < 0 ? 0 : L;
         it.s0 = seq_start(p, it.b, it.L);
         it.nparts = parts_of(it.L - it.s0, p.partition);
         it.part = it.nparts - 1;
+    }
+    if constexpr (WIN) {
+        const WindowSpan w = window_span(p, max(true_len(p, it.b), 0));
+        it.sinks = w.sinks;
+        it.lo = w.lo;
+        it.head = w.head;
+        it.skip = w.skip;
     }
     const int t0 = it.s0 + it.part * p.partition;
     it.t1 = min(it.L, t0 + p.partition);
     it.j0 = t0 / p.block_size;
     it.j1 = it.t1 > t0 ? (it.t1 + p.block_size - 1) / p.block_size : it.j0;
     return it;
+}
+
+// Windowed decode: position v of an item is seen by the query.
+template <bool WIN>
+__device__ __forceinline__ bool in_window(const Item& it, int v) {
+    if constexpr (WIN) return v >= it.lo || v < it.sinks;
+    return true;
+}
+// Every one of the n positions from v0 on is.
+template <bool WIN>
+__device__ __forceinline__ bool all_in_window(const Item& it, int v0, int n) {
+    if constexpr (WIN) return v0 >= it.lo || v0 + n <= it.sinks;
+    return true;
 }
 
 __device__ __forceinline__ float fast_exp2(float x) {
@@ -638,7 +698,7 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
 //    heads) the lo weights take a second MMA.
 // Masked tokens (past the item or on a missing page) get weight 0 and their
 // V rows are zeroed before the MMA, so stale stage bytes never reach a sum.
-template <typename C, int QDT, int KVDT, int D, int G, int BS>
+template <typename C, int QDT, int KVDT, int D, int G, int BS, bool WIN>
 __device__ __forceinline__ void decode_consumer_mma(const DecodeParams& p, uint8_t* ring, const uint8_t* qbuf,
                                                     float* merge, const int32_t* prefix, const int32_t* order,
                                                     int n_items, uint32_t full0, uint32_t empty0, uint32_t qfull0,
@@ -664,7 +724,7 @@ __device__ __forceinline__ void decode_consumer_mma(const DecodeParams& p, uint8
     const int S = p.stages;
     uint32_t stage = 0, phase = 0, fc = 0, qn = 0;
     for (int rnd = 0, i; (i = snake_item(rnd, n_items)) >= 0; ++rnd, ++qn) {
-        const Item it = decode_item(p, prefix, order, i);
+        const Item it = decode_item<WIN>(p, prefix, order, i);
         const uint32_t slot = qn & 1u;
         bool ok = __all_sync(0xffffffffu, mbar_wait(qfull0 + 8u * slot, (qn >> 1) & 1u, p.status, abort_flag));
         // ---- Q^T fragments: head gi, span [W*ti, W*ti + W) as pairs ----
@@ -736,11 +796,14 @@ __device__ __forceinline__ void decode_consumer_mma(const DecodeParams& p, uint8
                 const uint8_t* kr1 = kr0 + 8 * C::ROWB;
                 // a stage whose pages are all present and whose tokens all lie
                 // before the item's end needs no per-token masks
-                const bool full_stage = mask == (1 << C::SPAGES) - 1 && js * BS + C::STOK <= it.t1;
+                const bool full_stage = mask == (1 << C::SPAGES) - 1 && js * BS + C::STOK <= it.t1 &&
+                                        all_in_window<WIN>(it, js * BS, C::STOK);
                 auto slice = [&](auto full_tag) {
                     constexpr bool FULL = decltype(full_tag)::value;
-                    const bool v0 = FULL || (((mask >> (tk0 / BS)) & 1) && js * BS + tk0 < it.t1);
-                    const bool v1 = FULL || (((mask >> (tk1 / BS)) & 1) && js * BS + tk1 < it.t1);
+                    const bool v0 = FULL || (((mask >> (tk0 / BS)) & 1) && js * BS + tk0 < it.t1 &&
+                                             in_window<WIN>(it, js * BS + tk0));
+                    const bool v1 = FULL || (((mask >> (tk1 / BS)) & 1) && js * BS + tk1 < it.t1 &&
+                                             in_window<WIN>(it, js * BS + tk1));
                     // ---- S^T = K Q^T (two accumulators: two independent MMA chains) ----
                     float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
                     if constexpr (C::KB == 2) {
@@ -987,13 +1050,15 @@ __device__ __forceinline__ void append_row(const DecodeParams& p, const Item& it
     }
 }
 
-// APPEND: the new token of every sequence is written and attended in the
-// same launch (pa_decode_append); a separate instantiation keeps the plain
-// decode's producer loop as lean as it was.
-template <int QDT, int KVDT, int D, int G, int BS, bool APPEND>
+// MODE: kAppend writes and attends the new token of every sequence in the same
+// launch (pa_decode_append), kWindow attends the sinks' and the window's blocks
+// (pa_decode_window); instantiations of their own keep the plain decode's loops
+// as lean as they were.
+template <int QDT, int KVDT, int D, int G, int BS, int MODE>
 __global__ void __maxnreg__((DecodeCfg<QDT, KVDT, D, G, BS>::MAX_REGS))
 paged_decode_kernel(const DecodeParams p) {
     using C = DecodeCfg<QDT, KVDT, D, G, BS>;
+    constexpr bool APPEND = MODE == kAppend, WIN = MODE == kWindow;
     // the 16-bit type the QK products are taken in: the cache's, or fp16
     // (exact for E4M3 codes) with power-of-two scaled queries for E4M3 caches
     constexpr int KT = C::KB == 2 ? KVDT : PA_F16;
@@ -1028,7 +1093,7 @@ paged_decode_kernel(const DecodeParams p) {
     }
     // merge area doubles as scan scratch before the first item
     int32_t* order = reinterpret_cast<int32_t*>(smem_raw + L.order);
-    build_schedule(p, prefix, order, reinterpret_cast<int32_t*>(merge), smem_raw + L.keys,
+    build_schedule<WIN>(p, prefix, order, reinterpret_cast<int32_t*>(merge), smem_raw + L.keys,
                    reinterpret_cast<int32_t*>(smem_raw + L.hist));
     const int n_items = (prefix[p.num_seqs] + p.num_seqs) * p.num_kv_heads;
 
@@ -1043,7 +1108,7 @@ paged_decode_kernel(const DecodeParams p) {
         uint32_t qn = 0;      // items issued so far
         bool ok = true;
         for (int rnd = 0, i; ok && (i = snake_item(rnd, n_items)) >= 0; ++rnd, ++qn) {
-            const Item it = decode_item(p, prefix, order, i);
+            const Item it = decode_item<WIN>(p, prefix, order, i);
             if (lane == 0) {
                 const uint32_t slot = qn & 1u;
                 if (qn >= 2) ok = mbar_wait(qempty0 + 8u * slot, ((qn >> 1) - 1) & 1u, p.status, abort_flag);
@@ -1095,13 +1160,12 @@ paged_decode_kernel(const DecodeParams p) {
             // block ids come 32 at a time, one per lane; the next batch's load
             // is issued before this batch's stages are filled, so its latency
             // hides behind them
-            // block ids come 32 at a time, one per lane; the next batch's load
-            // is issued before this batch's stages are filled, so its latency
-            // hides behind them
-            int32_t id_next = it.j0 + lane < it.j1 ? __ldg(row + it.j0 + lane) : -1;
+            // (windowed decode: past the sinks' blocks the row is read `skip` entries on)
+            auto entry = [&](int j) { return WIN && j >= it.head ? j + it.skip : j; };
+            int32_t id_next = it.j0 + lane < it.j1 ? __ldg(row + entry(it.j0 + lane)) : -1;
             for (int jb = it.j0; jb < it.j1 && ok; jb += 32) {
                 const int32_t id = id_next;
-                id_next = jb + 32 + lane < it.j1 ? __ldg(row + jb + 32 + lane) : -1;
+                id_next = jb + 32 + lane < it.j1 ? __ldg(row + entry(jb + 32 + lane)) : -1;
                 const int cnt = min(32, it.j1 - jb);
                 for (int k0 = 0; k0 < cnt; k0 += C::SPAGES) {
                     int32_t ids[C::SPAGES];
@@ -1229,7 +1293,7 @@ paged_decode_kernel(const DecodeParams p) {
 
     // ------------------------------- consumers ------------------------------
     if constexpr (C::MMA) {
-        decode_consumer_mma<C, QDT, KVDT, D, G, BS>(p, ring, qbuf, merge, prefix, order, n_items, full0, empty0,
+        decode_consumer_mma<C, QDT, KVDT, D, G, BS, WIN>(p, ring, qbuf, merge, prefix, order, n_items, full0, empty0,
                                                     qfull0, qempty0, abort_flag, stage_mask, warp, lane);
         return;
     }
@@ -1248,7 +1312,7 @@ paged_decode_kernel(const DecodeParams p) {
     uint32_t stage = 0, phase = 0;
     uint32_t qn = 0;
     for (int rnd = 0, i; (i = snake_item(rnd, n_items)) >= 0; ++rnd, ++qn) {
-        const Item it = decode_item(p, prefix, order, i);
+        const Item it = decode_item<WIN>(p, prefix, order, i);
         const uint32_t slot = qn & 1u;
         bool ok = __all_sync(0xffffffffu, mbar_wait(qfull0 + 8u * slot, (qn >> 1) & 1u, p.status, abort_flag));
         // this warp's queries as packed 16-bit pairs in the lane's chunk order
@@ -1323,7 +1387,8 @@ paged_decode_kernel(const DecodeParams p) {
             const int tok0 = js * BS + tw * C::TG + tg;  // this group's first position
             // a stage whose pages are all present and whose tokens all lie
             // before the item's end takes a path without per-token masks
-            const bool full_stage = mask == (1 << C::SPAGES) - 1 && js * BS + C::STOK <= it.t1;
+            const bool full_stage = mask == (1 << C::SPAGES) - 1 && js * BS + C::STOK <= it.t1 &&
+                                    all_in_window<WIN>(it, js * BS, C::STOK);
             auto stage_steps = [&](auto full_tag) {
                 constexpr bool FULL = decltype(full_tag)::value;
                 // with several heads per warp, steps go in pairs (NB = 2): both
@@ -1338,7 +1403,8 @@ paged_decode_kernel(const DecodeParams p) {
 #pragma unroll
                     for (int h = 0; h < C::NB; ++h) {
                         const int tis = (u0 + h) * C::TPI;  // step offset inside the stage
-                        valid[h] = FULL || (((mask >> ((tis + tw * C::TG + tg) / BS)) & 1) && tok0 + tis < it.t1);
+                        valid[h] = FULL || (((mask >> ((tis + tw * C::TG + tg) / BS)) & 1) && tok0 + tis < it.t1 &&
+                                            in_window<WIN>(it, tok0 + tis));
                         // value chunks are loaded up front (unconditionally: the
                         // rows are in shared memory) so the loads overlap the QK math
 #pragma unroll
@@ -1512,7 +1578,7 @@ paged_decode_kernel(const DecodeParams p) {
 // shared memory.  Lanes own D/32 consecutive output columns.  With hundreds of
 // partitions per pair (long contexts) one warp per pair left most of the GPU
 // idle and each warp waiting on one row load at a time.
-template <int QDT, int D, int WPP>
+template <int QDT, int D, int WPP, bool WIN>
 __global__ void __launch_bounds__(256)
 paged_decode_reduce_kernel(const DecodeParams p) {
     pdl_wait();
@@ -1526,7 +1592,7 @@ paged_decode_reduce_kernel(const DecodeParams p) {
     int np = 0;
     if (bh < static_cast<int64_t>(p.num_seqs) * p.num_heads) {
         const int b = static_cast<int>(bh / p.num_heads);
-        const int Lc = checked_len(p, b);
+        const int Lc = checked_len<WIN>(p, b);
         const int L = Lc < 0 ? 0 : Lc;
         // cascade: the prefix's parts, then the suffix's partitions
         const int s0 = seq_start(p, b, L);

@@ -32,10 +32,12 @@ pa_status launch_decode_t(DecodeParams p, cudaStream_t stream) {
     const DecodeSmem L = DecodeSmem::make(p.stages, C::STAGE_BYTES, C::QBYTES, C::MERGE_FLOATS, p.num_seqs);
     const int smem = static_cast<int>(L.total) + 1024;  // slack for the 1 KB base alignment
     if (smem > device_max_smem_optin()) return PA_ERR_UNSUPPORTED;
-    const bool append = p.k_new != nullptr;
-    auto kern = append ? paged_decode_kernel<QDT, KVDT, D, G, BS, true> : paged_decode_kernel<QDT, KVDT, D, G, BS, false>;
-    static LaunchCache cache, cache_append;
-    const int per_sm = blocks_per_sm(kern, C::THREADS, smem, append ? cache_append : cache);
+    const int mode = p.window > 0 ? kWindow : p.k_new != nullptr ? kAppend : kPlain;
+    auto kern = mode == kWindow   ? paged_decode_kernel<QDT, KVDT, D, G, BS, kWindow>
+                : mode == kAppend ? paged_decode_kernel<QDT, KVDT, D, G, BS, kAppend>
+                                  : paged_decode_kernel<QDT, KVDT, D, G, BS, kPlain>;
+    static LaunchCache caches[3];
+    const int per_sm = blocks_per_sm(kern, C::THREADS, smem, caches[mode]);
     if (per_sm <= 0) return PA_ERR_CUDA;
     const int sms = device_sm_count();
     const int64_t max_items = static_cast<int64_t>(p.num_seqs) * p.num_kv_heads * p.max_parts;
@@ -54,11 +56,14 @@ pa_status launch_decode_t(DecodeParams p, cudaStream_t stream) {
         const int64_t pairs = static_cast<int64_t>(r.num_seqs) * r.num_heads;
         const int wpp = p.max_parts >= 32 ? 8 : p.max_parts >= 8 ? 4 : p.max_parts >= 3 ? 2 : 1;
         const int rgrid = static_cast<int>((pairs * wpp + 7) / 8);
-        cudaError_t e;
-        if (wpp == 8) e = launch_pdl(paged_decode_reduce_kernel<QDT, D, 8>, rgrid, 256, 0, stream, r);
-        else if (wpp == 4) e = launch_pdl(paged_decode_reduce_kernel<QDT, D, 4>, rgrid, 256, 0, stream, r);
-        else if (wpp == 2) e = launch_pdl(paged_decode_reduce_kernel<QDT, D, 2>, rgrid, 256, 0, stream, r);
-        else e = launch_pdl(paged_decode_reduce_kernel<QDT, D, 1>, rgrid, 256, 0, stream, r);
+        auto reduce = [&](auto win) {
+            constexpr bool WIN = decltype(win)::value;
+            if (wpp == 8) return launch_pdl(paged_decode_reduce_kernel<QDT, D, 8, WIN>, rgrid, 256, 0, stream, r);
+            if (wpp == 4) return launch_pdl(paged_decode_reduce_kernel<QDT, D, 4, WIN>, rgrid, 256, 0, stream, r);
+            if (wpp == 2) return launch_pdl(paged_decode_reduce_kernel<QDT, D, 2, WIN>, rgrid, 256, 0, stream, r);
+            return launch_pdl(paged_decode_reduce_kernel<QDT, D, 1, WIN>, rgrid, 256, 0, stream, r);
+        };
+        const cudaError_t e = mode == kWindow ? reduce(std::true_type{}) : reduce(std::false_type{});
         if (e != cudaSuccess) return PA_ERR_CUDA;
     }
     return PA_OK;
