@@ -359,6 +359,24 @@ pa_status pa_prefill_varlen(void* out, const void* q, pa_dtype q_dtype, const pa
                             pa_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Varlen prefill with a sliding window and sinks: pa_prefill_varlen, causal, with
+ * pa_decode_window's mask.  Query i of a sequence, at position x = Lk - Lq + i, sees
+ * the keys
+ *     j <= x   with   j > x - window   or   j < num_sinks.
+ * A window of max_seqlen_k or more gives pa_prefill_varlen's causal result.
+ * Block-table entries of blocks that no query of the sequence sees are not read,
+ * and positions that none of them sees may hold anything (NaN included).  A value
+ * that some query sees has to be finite for the other queries of the sequence too
+ * (a weight of zero still multiplies it).
+ * scale > 0.  Everything else as pa_prefill_varlen (head_size 128).
+ * ------------------------------------------------------------------------- */
+pa_status pa_prefill_varlen_window(void* out, const void* q, pa_dtype q_dtype, const pa_kv_cache* cache,
+                                   const int32_t* block_table, int32_t max_blocks_per_seq,
+                                   const int32_t* cu_seq_lens_q, const int32_t* cu_seq_lens_k, int32_t num_seqs,
+                                   int32_t max_seqlen_q, int32_t max_seqlen_k, int32_t num_heads, float scale,
+                                   int32_t window, int32_t num_sinks, int32_t* dev_status, pa_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Swap whole blocks between the device cache and page-locked host memory:
  * the data move of swap-based preemption ("Как работает paged attention?"
  * 4.3: the preempted request's KV cache goes to CPU memory and comes back

@@ -64,6 +64,8 @@ def library():
                                  C.c_int),
             "pa_prefill_varlen": ([vp, vp, C.c_int, pc, vp, i32, vp, vp, i32, i32, i32, i32, f32, i32,
                                    vp, vp], C.c_int),
+            "pa_prefill_varlen_window": ([vp, vp, C.c_int, pc, vp, i32, vp, vp, i32, i32, i32, i32, f32, i32, i32, vp,
+                                          vp], C.c_int),
             "pa_pool_create": ([i64, i32, vp, C.POINTER(vp)], C.c_int),
             "pa_pool_destroy": ([vp], None),
             "pa_pool_add_seq": ([vp, i64], C.c_int),
@@ -646,6 +648,36 @@ def pa_prefill_varlen(out: torch.Tensor, q: torch.Tensor, cache: KVCache, block_
                                      _ptr(cu_seq_lens_k), B, int(max_seqlen_q), int(max_seqlen_k), H,
                                      float(scale), 1 if causal else 0, _ptr(dev_status), _stream(q))
     _check(st, "pa_prefill_varlen")
+
+
+def pa_prefill_varlen_window(out: torch.Tensor, q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
+                             cu_seq_lens_q: torch.Tensor, cu_seq_lens_k: torch.Tensor, max_seqlen_q: int,
+                             max_seqlen_k: int, scale: float, window: int, num_sinks: int = 0,
+                             dev_status: Optional[torch.Tensor] = None):
+    """pa_prefill_varlen, causal, where a query at position x sees the keys of
+    positions x - window + 1 .. x and the first num_sinks; block-table entries
+    of blocks that no query sees are not read."""
+    _need(q, "q")
+    _need(out, "out", q.dtype)
+    _need(block_table, "block_table", torch.int32)
+    _need(cu_seq_lens_q, "cu_seq_lens_q", torch.int32)
+    _need(cu_seq_lens_k, "cu_seq_lens_k", torch.int32)
+    dev = q.device
+    B = cu_seq_lens_q.shape[0] - 1
+    if q.dim() != 3 or out.shape != q.shape or block_table.dim() != 2 or block_table.shape[0] != B or \
+            cu_seq_lens_k.shape != cu_seq_lens_q.shape or q.shape[2] != cache.head_size:
+        raise ValueError("out must have q's shape [total_q, num_heads, head_size], block_table [num_seqs, max_blocks], "
+                         "cu_seq_lens_q and _k [num_seqs + 1], the cache q's head size")
+    _same_device(dev, out=out, cache=cache.k_cache, block_table=block_table, cu_seq_lens_q=cu_seq_lens_q,
+                 cu_seq_lens_k=cu_seq_lens_k)
+    with _on(dev):
+        st = library().pa_prefill_varlen_window(out.data_ptr(), q.data_ptr(), torch_dtype_code(q.dtype),
+                                                cache.c_struct(), block_table.data_ptr(), block_table.shape[1],
+                                                cu_seq_lens_q.data_ptr(), cu_seq_lens_k.data_ptr(), B,
+                                                int(max_seqlen_q), int(max_seqlen_k), q.shape[1], float(scale),
+                                                int(window), int(num_sinks), _status_ptr(dev_status, dev),
+                                                _raw_stream(dev))
+    _check(st, "pa_prefill_varlen_window")
 
 
 def pa_slot_mapping(block_table, block_size: int, seq_idx, pos):

@@ -44,7 +44,9 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <cmath>
 #include <mutex>
+#include <type_traits>
 
 #include "common.cuh"
 #include "launch.h"
@@ -106,6 +108,32 @@ struct PrefillParams {
     int32_t order_cap; // query tiles the shared-memory work order holds (set by the launch)
     int32_t q_rows;    // token extent of the query tensor map: min(num_seqs * max_seqlen_q, INT32_MAX)
 };
+
+// Sliding window (pa_prefill_varlen_window): a query sees the last `window`
+// positions up to its own and the first `sinks`, which lie in `head` blocks.
+// (Fields of their own: three more in the plain launches' parameters made the
+// compiler spill 20 bytes more in their softmax.)
+struct WindowParams : PrefillParams {
+    int32_t window, sinks, head;
+};
+template <bool WIN>
+using ParamsOf = std::conditional_t<WIN, WindowParams, PrefillParams>;
+template <bool WIN>
+__device__ __forceinline__ int sinks_of(const ParamsOf<WIN>& p) {
+    if constexpr (WIN) return p.sinks;
+    else return 0;
+}
+template <bool WIN>
+__device__ __forceinline__ int head_of(const ParamsOf<WIN>& p) {
+    if constexpr (WIN) return p.head;
+    else return 0;
+}
+// first position that a query at position `pos` sees through the window
+template <bool WIN>
+__device__ __forceinline__ int first_key(const ParamsOf<WIN>& p, int pos) {
+    if constexpr (WIN) return max(0, pos - p.window + 1);
+    else return 0;
+}
 
 // ---------------------------------------------------------------------------
 // PTX wrappers (tcgen05, TMA)
@@ -327,10 +355,30 @@ __device__ __forceinline__ bool seq_lens_ok(const PrefillParams& p, int b, int& 
 }
 
 struct Work {
-    int b, i0, kvh, lq, lk, kend, ntiles;
+    int b, i0, kvh, lq, lk, ntiles;
+    int skip;  // sliding window: blocks left out between the sinks' and the window's
     int q0;  // cu_q[b]: the sequence's first query row
 };
 static_assert(sizeof(Work) == 32, "the item cache holds 32-byte entries");
+
+// What an item's queries i0 .. min(i0 + tq, lq) - 1 see lies in keys 0 .. kend-1
+// and, with a sliding window (WIN), from these without the blocks between the
+// sinks' `head` and the window of the item's first query: the item works on the
+// blocks that are left as if they were all, position v standing for v + skip *
+// block_size past the sinks' blocks.  A row then sees v < sinks and lo <= v < lim
+// with its own lo and lim in those positions (skip > 0: the sinks' last block
+// ends at or before every row's lo).
+template <bool WIN>
+__device__ __forceinline__ int key_tiles(const ParamsOf<WIN>& p, int i0, int lq, int lk, int& skip) {
+    int kend = lk;
+    if (WIN || p.causal) kend = min(lk, lk - lq + min(i0 + p.tq, lq));
+    skip = 0;
+    if constexpr (WIN) {
+        skip = max(0, first_key<WIN>(p, lk - lq + i0) / p.block_size - p.head);
+        kend -= skip * p.block_size;
+    }
+    return kend > 0 ? (kend + kBN - 1) / kBN : 0;
+}
 
 // Work order.  An item's cost is its number of key tiles, which under the
 // causal mask grows along a sequence's query tiles and differs widely between
@@ -350,15 +398,22 @@ __device__ __forceinline__ int tile_seq(const PrefillParams& p, const int32_t* p
     return lo;
 }
 
-__device__ __forceinline__ int tile_class(const PrefillParams& p, const int32_t* prefix, int tile) {
+template <bool WIN>
+__device__ __forceinline__ int tile_class(const ParamsOf<WIN>& p, const int32_t* prefix, int tile) {
     const int b = tile_seq(p, prefix, tile);
     int lq, lk;
     seq_lens_ok(p, b, lq, lk);
     const int i0 = (tile - prefix[b]) * p.tq;
-    int kend = lk;
-    if (p.causal) kend = min(lk, lk - lq + min(i0 + p.tq, lq));
-    const int maxt = (p.max_k + kBN - 1) / kBN;
-    const int nt = kend > 0 ? min(maxt, (kend + kBN - 1) / kBN) : 0;
+    int skip;
+    int most = p.max_k;
+    if constexpr (WIN) {
+        // (the most keys of an item: the sinks' blocks, the window, the item's
+        // other queries, the rest of the window's first block)
+        const int64_t span = static_cast<int64_t>(p.head + 1) * p.block_size + p.window + p.tq;
+        most = static_cast<int>(min(span, static_cast<int64_t>(most)));
+    }
+    const int maxt = (most + kBN - 1) / kBN;
+    const int nt = min(maxt, key_tiles<WIN>(p, i0, lq, lk, skip));
     return 63 - static_cast<int>((static_cast<int64_t>(nt) * 64) / (maxt + 1));  // 0 = most key tiles
 }
 
@@ -366,7 +421,8 @@ __device__ __forceinline__ int tile_class(const PrefillParams& p, const int32_t*
 // contiguous chunk (lanes of equal class found by match.any), warp 0 turns
 // the [warp][class] counts into class-major offsets, each warp then places its
 // chunk in order.  All threads of the block take part; hist holds 12*64 ints.
-__device__ void build_tile_order(const PrefillParams& p, const int32_t* prefix, int n, int32_t* order,
+template <bool WIN>
+__device__ void build_tile_order(const ParamsOf<WIN>& p, const int32_t* prefix, int n, int32_t* order,
                                  int32_t* hist) {
     constexpr int NW = kThreads / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -378,7 +434,7 @@ __device__ void build_tile_order(const PrefillParams& p, const int32_t* prefix, 
     __syncwarp();
     for (int c0 = t0; c0 < t1; c0 += 32) {
         const int t = c0 + lane;
-        const int key = t < t1 ? tile_class(p, prefix, t) : 64;
+        const int key = t < t1 ? tile_class<WIN>(p, prefix, t) : 64;
         const unsigned same = __match_any_sync(0xffffffffu, key);
         if (t < t1 && lane == __ffs(same) - 1) h[key] += __popc(same);
         __syncwarp();
@@ -408,7 +464,7 @@ __device__ void build_tile_order(const PrefillParams& p, const int32_t* prefix, 
     __syncthreads();
     for (int c0 = t0; c0 < t1; c0 += 32) {
         const int t = c0 + lane;
-        const int key = t < t1 ? tile_class(p, prefix, t) : 64;
+        const int key = t < t1 ? tile_class<WIN>(p, prefix, t) : 64;
         const unsigned same = __match_any_sync(0xffffffffu, key);
         if (t < t1) order[h[key] + __popc(same & ((1u << lane) - 1u))] = t;
         __syncwarp();
@@ -418,7 +474,8 @@ __device__ void build_tile_order(const PrefillParams& p, const int32_t* prefix, 
     __syncthreads();
 }
 
-__device__ __forceinline__ Work work_item(const PrefillParams& p, const int32_t* prefix, const int32_t* order,
+template <bool WIN>
+__device__ __forceinline__ Work work_item(const ParamsOf<WIN>& p, const int32_t* prefix, const int32_t* order,
                                           int item) {
     Work w;
     int tile_id = item / p.num_kv_heads;
@@ -434,20 +491,36 @@ __device__ __forceinline__ Work work_item(const PrefillParams& p, const int32_t*
     seq_lens_ok(p, lo, w.lq, w.lk);
     w.q0 = __ldg(p.cu_q + lo);
     w.i0 = (tile_id - prefix[lo]) * p.tq;
-    const int shift = w.lk - w.lq;
-    w.kend = w.lk;
-    if (p.causal) w.kend = min(w.lk, shift + min(w.i0 + p.tq, w.lq));
-    w.ntiles = w.kend > 0 ? (w.kend + kBN - 1) / kBN : 0;
+    w.ntiles = key_tiles<WIN>(p, w.i0, w.lq, w.lk, w.skip);
     return w;
+}
+
+// scores of keys that are not seen: those from vis on, and (WIN) [hid0, hid1)
+template <bool WIN>
+__device__ __forceinline__ void hide_keys(float (&e)[64], int vis, int hid0, int hid1) {
+    if (vis < 64) {
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+            if (i >= vis) e[i] = -INFINITY;
+    }
+    if constexpr (WIN) {
+        if (hid0 < hid1) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+                if (i >= hid0 && i < hid1) e[i] = -INFINITY;
+        }
+    }
 }
 
 // PACKED: K and V are contiguous [Σk][num_kv_heads][head_size] tensors indexed
 // by cu_seq_lens_k (no cache, no block table); otherwise the paged cache.
-template <int DT, bool PACKED>
+// WIN: causal with a sliding window and sinks (an instantiation of its own, so
+// that the others' softmax carries no second mask).
+template <int DT, bool PACKED, bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                         const __grid_constant__ CUtensorMap map_q,
-                        const PrefillParams p) {
+                        const ParamsOf<WIN> p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     // 128B-swizzled tiles need 1 KB alignment; the launch adds 1 KB of slack
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -549,7 +622,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
     const int32_t* order = nullptr;
     if (p.order_cap > 0 && prefix[B] <= p.order_cap) {
         int32_t* ord = prefix + B + 1;
-        build_tile_order(p, prefix, prefix[B], ord, ord + p.order_cap);
+        build_tile_order<WIN>(p, prefix, prefix[B], ord, ord + p.order_cap);
         order = ord;
     }
     const uint32_t tmem = *tmem_slot;
@@ -560,11 +633,11 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
     Work* item_cache = reinterpret_cast<Work*>(smem + kOffItems);
     if (tid < kItemCache) {
         const int item = snake_item(tid, n_items);
-        if (item >= 0) item_cache[tid] = work_item(p, prefix, order, item);
+        if (item >= 0) item_cache[tid] = work_item<WIN>(p, prefix, order, item);
     }
     __syncthreads();
     auto item_work = [&](int rnd, int item) -> Work {
-        return rnd < kItemCache ? item_cache[rnd] : work_item(p, prefix, order, item);
+        return rnd < kItemCache ? item_cache[rnd] : work_item<WIN>(p, prefix, order, item);
     };
     if (warp == 0 || warp == 2) {
         // ------------------------------- loaders -------------------------------
@@ -620,9 +693,10 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
                     const int pg0 = t * ppt;  // first page of this tile
                     if ((pg0 & 31) == 0) {
                         const int pg = pg0 + lane;
+                        const int entry = WIN && pg >= head_of<WIN>(p) ? pg + w.skip : pg;
                         id = -1;
-                        if (pg < pages && pg * p.block_size < w.lk) {
-                            id = __ldg(bt_row + pg);
+                        if (pg < pages && entry * p.block_size < w.lk) {
+                            id = __ldg(bt_row + entry);
                             if (id < 0 || id >= p.num_blocks) {
                                 // both loader warps read the id; one reports it
                                 if (kv == 0) report(p.status, PA_ERR_BAD_BLOCK);
@@ -931,7 +1005,13 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
             const int qi = w.i0 + t_row;  // query index of this row in its sequence
             bool row_valid;
             const int64_t row_off = row_of(w, row_valid);
-            const int lim = p.causal ? min(w.lk, shift + qi + 1) : w.lk;  // keys [0, lim) visible
+            // keys [0, lim) visible (window: of these, none from the sinks' end to
+            // lo; for the item's rows together, to lo_item)
+            const int gone = WIN ? w.skip * p.block_size : 0;
+            const int lk = w.lk - gone;
+            const int lim = (WIN || p.causal ? min(w.lk, shift + qi + 1) : w.lk) - gone;
+            [[maybe_unused]] const int lo = first_key<WIN>(p, shift + qi) - gone;
+            [[maybe_unused]] const int lo_item = first_key<WIN>(p, shift + w.i0) - gone;
             uint16_t* dst = static_cast<uint16_t*>(p.out) + row_off + 64 * x;
             if (w.ntiles == 0) {
                 // no visible key for any row of the item: output 0
@@ -956,6 +1036,9 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
                 const int b = t & 1;
                 const int key0 = t * kBN + 64 * x;  // first key of this thread's 64 columns
                 const int vis = row_valid ? lim - key0 : 0;  // visible keys of these columns: [0, vis)
+                // ... without [hid0, hid1)
+                [[maybe_unused]] const int hid0 = WIN ? max(sinks_of<WIN>(p) - key0, 0) : 0;
+                [[maybe_unused]] const int hid1 = WIN ? min(lo - key0, 64) : 0;
                 ok = ok && mbar_wait(s_full + 8 * b, s_use[b] & 1u, p.status, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 ++s_use[b];
@@ -965,15 +1048,11 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
                 if (ok) {
                     tc_fence_after();
                     tmem_ld64(sbuf + b * kBN, e);
-                    if (vis < 64) {
-#pragma unroll
-                        for (int i = 0; i < 64; ++i)
-                            if (i >= vis) e[i] = -INFINITY;
-                    }
+                    hide_keys<WIN>(e, vis, hid0, hid1);
                     if (m == -INFINITY) {
                         // no reference yet: the slow path, unless these columns
                         // are all masked for this row (weights 0)
-                        over = vis > 0;
+                        over = vis > 0 && !(WIN && hid0 == 0 && hid1 >= min(vis, 64));
 #pragma unroll
                         for (int i = 0; i < 64; ++i) e[i] = 0.f;
                     } else {
@@ -1011,11 +1090,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
                     float mx = -INFINITY;
                     if (ok) {
                         tmem_ld64(sbuf + b * kBN, e);
-                        if (vis < 64) {
-#pragma unroll
-                            for (int i = 0; i < 64; ++i)
-                                if (i >= vis) e[i] = -INFINITY;
-                        }
+                        hide_keys<WIN>(e, vis, hid0, hid1);
                         float m8[8];
 #pragma unroll
                         for (int j = 0; j < 8; ++j) m8[j] = fmax3(e[8 * j], e[8 * j + 1], e[8 * j + 2]);
@@ -1079,19 +1154,26 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
                 if (!ok) continue;
                 l += sum;
                 // values past Lk in the last tile may hold anything: zero those
-                // V rows (after the tile landed) so zero weights never meet NaN
-                if (t * kBN + kBN > w.lk) {
+                // V rows (after the tile landed) so zero weights never meet NaN;
+                // window: also those that no row of the item sees, from the sinks'
+                // end to the first row's lo
+                const int hole0 = WIN ? max(sinks_of<WIN>(p) - t * kBN, 0) : 0;
+                const int hole1 = WIN ? min(lo_item - t * kBN, kBN) : 0;
+                if (t * kBN + kBN > lk || (WIN && hole0 < hole1)) {
                     const uint32_t f = tiles + t;
                     ok = mbar_wait(v_full + 8 * (f % kStagesV), (f / kStagesV) & 1u, p.status, abort_flag);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) continue;
                     uint8_t* vt = sV + (f % kStagesV) * kTileBytes;
-                    const int first = max(0, w.lk - t * kBN);
-                    for (int ci = u; ci < (kBN - first) * 16; ci += 256) {
-                        const int rr = first + (ci >> 4), c = ci & 15;
-                        *reinterpret_cast<uint4*>(vt + (c >> 3) * kBlkBytes + sw128(rr, c & 7)) =
-                            make_uint4(0u, 0u, 0u, 0u);
-                    }
+                    auto zero_rows = [&](int first, int end) {
+                        for (int ci = u; ci < (end - first) * 16; ci += 256) {
+                            const int rr = first + (ci >> 4), c = ci & 15;
+                            *reinterpret_cast<uint4*>(vt + (c >> 3) * kBlkBytes + sw128(rr, c & 7)) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                        }
+                    };
+                    zero_rows(max(0, lk - t * kBN), kBN);
+                    if constexpr (WIN) zero_rows(hole0, hole1);
                     fence_async_smem();
                 }
                 // P over S in tensor memory as 16-bit pairs (bf16: hi at columns
@@ -1214,8 +1296,8 @@ bool make_q_map(CUtensorMap* map, const void* q, int num_heads, int group, int n
 }
 
 // launch shared by the paged and packed entry points (p filled in, maps built)
-template <bool PACKED>
-pa_status launch_prefill(const PrefillParams& p, pa_dtype dtype, const CUtensorMap& map_k,
+template <bool PACKED, bool WIN>
+pa_status launch_prefill(const ParamsOf<WIN>& p, pa_dtype dtype, const CUtensorMap& map_k,
                          const CUtensorMap& map_v, const CUtensorMap& map_q, pa_stream_t stream) {
     // shared memory past the fixed layout: the tile prefix (B+1 ints), the
     // work order (up to every query tile the bounds allow, within what the
@@ -1225,11 +1307,12 @@ pa_status launch_prefill(const PrefillParams& p, pa_dtype dtype, const CUtensorM
     const int64_t tiles_bound = static_cast<int64_t>(p.num_seqs) * ((p.max_q + p.tq - 1) / p.tq);
     // (2 KB kept back for the kernel's static shared memory)
     const int64_t room = (device_max_smem_optin() - 2048 - base) / 4 - (kThreads / 32) * 64;
-    PrefillParams q = p;
+    ParamsOf<WIN> q = p;
     q.order_cap = static_cast<int32_t>(room <= 0 ? 0 : (tiles_bound < room ? tiles_bound : room));
     const int smem = base + (q.order_cap > 0 ? (q.order_cap + (kThreads / 32) * 64) * 4 : 0);
     static LaunchCache cache_bf16, cache_f16;
-    auto kern = dtype == PA_BF16 ? paged_prefill_tc_kernel<PA_BF16, PACKED> : paged_prefill_tc_kernel<PA_F16, PACKED>;
+    auto kern = dtype == PA_BF16 ? paged_prefill_tc_kernel<PA_BF16, PACKED, WIN>
+                                : paged_prefill_tc_kernel<PA_F16, PACKED, WIN>;
     const int per_sm = blocks_per_sm(kern, kThreads, smem, dtype == PA_BF16 ? cache_bf16 : cache_f16);
     if (per_sm <= 0) return PA_ERR_CUDA;
     const int64_t max_items =
@@ -1248,13 +1331,15 @@ pa_status launch_prefill(const PrefillParams& p, pa_dtype dtype, const CUtensorM
 
 using namespace pa;
 
-extern "C" pa_status pa_prefill_varlen(void* out, const void* q, pa_dtype q_dtype,
-                                       const pa_kv_cache* cache, const int32_t* block_table,
-                                       int32_t max_blocks_per_seq, const int32_t* cu_seq_lens_q,
-                                       const int32_t* cu_seq_lens_k, int32_t num_seqs,
-                                       int32_t max_seqlen_q, int32_t max_seqlen_k, int32_t num_heads,
-                                       float scale, int32_t causal, int32_t* dev_status,
-                                       pa_stream_t stream) {
+namespace pa {
+namespace {
+
+// pa_prefill_varlen, and pa_prefill_varlen_window when window > 0
+pa_status prefill_entry(void* out, const void* q, pa_dtype q_dtype, const pa_kv_cache* cache,
+                        const int32_t* block_table, int32_t max_blocks_per_seq, const int32_t* cu_seq_lens_q,
+                        const int32_t* cu_seq_lens_k, int32_t num_seqs, int32_t max_seqlen_q, int32_t max_seqlen_k,
+                        int32_t num_heads, float scale, int32_t causal, int32_t window, int32_t sinks,
+                        int32_t* dev_status, pa_stream_t stream) {
     pa_status st = check_cache(cache);
     if (st != PA_OK) return st;
     if (num_seqs < 0 || num_heads <= 0 || max_blocks_per_seq <= 0 || max_seqlen_q < 0 ||
@@ -1306,7 +1391,42 @@ extern "C" pa_status pa_prefill_varlen(void* out, const void* q, pa_dtype q_dtyp
     CUtensorMap map_q;
     if (!make_q_map(&map_q, q, num_heads, group, num_seqs, max_seqlen_q, q_dtype)) return PA_ERR_CUDA;
     p.q_rows = q_map_rows(num_seqs, max_seqlen_q);
-    return launch_prefill<false>(p, q_dtype, map_k, map_v, map_q, stream);
+    if (window > 0) {
+        // (a window, or sinks, past the longest sequence change nothing more)
+        const int32_t most = max_seqlen_k > 1 ? max_seqlen_k : 1;
+        WindowParams w{p, window < most ? window : most, sinks < most ? sinks : most, 0};
+        w.head = (w.sinks + bs - 1) / bs;
+        return launch_prefill<false, true>(w, q_dtype, map_k, map_v, map_q, stream);
+    }
+    return launch_prefill<false, false>(p, q_dtype, map_k, map_v, map_q, stream);
+}
+
+}  // namespace
+}  // namespace pa
+
+extern "C" pa_status pa_prefill_varlen(void* out, const void* q, pa_dtype q_dtype,
+                                       const pa_kv_cache* cache, const int32_t* block_table,
+                                       int32_t max_blocks_per_seq, const int32_t* cu_seq_lens_q,
+                                       const int32_t* cu_seq_lens_k, int32_t num_seqs,
+                                       int32_t max_seqlen_q, int32_t max_seqlen_k, int32_t num_heads,
+                                       float scale, int32_t causal, int32_t* dev_status,
+                                       pa_stream_t stream) {
+    return pa::prefill_entry(out, q, q_dtype, cache, block_table, max_blocks_per_seq, cu_seq_lens_q, cu_seq_lens_k,
+                             num_seqs, max_seqlen_q, max_seqlen_k, num_heads, scale, causal, 0, 0, dev_status, stream);
+}
+
+extern "C" pa_status pa_prefill_varlen_window(void* out, const void* q, pa_dtype q_dtype, const pa_kv_cache* cache,
+                                              const int32_t* block_table, int32_t max_blocks_per_seq,
+                                              const int32_t* cu_seq_lens_q, const int32_t* cu_seq_lens_k,
+                                              int32_t num_seqs, int32_t max_seqlen_q, int32_t max_seqlen_k,
+                                              int32_t num_heads, float scale, int32_t window, int32_t num_sinks,
+                                              int32_t* dev_status, pa_stream_t stream) {
+    if (window <= 0 || num_sinks < 0) return PA_ERR_INVALID_ARG;
+    // (the running maximum is taken over unscaled scores)
+    if (!(scale > 0.f) || !std::isfinite(scale)) return PA_ERR_INVALID_ARG;
+    return pa::prefill_entry(out, q, q_dtype, cache, block_table, max_blocks_per_seq, cu_seq_lens_q, cu_seq_lens_k,
+                             num_seqs, max_seqlen_q, max_seqlen_k, num_heads, scale, 1, window, num_sinks, dev_status,
+                             stream);
 }
 
 extern "C" pa_status pa_prefill_varlen_packed(void* out, const void* q, const void* k, const void* v,
@@ -1361,5 +1481,5 @@ extern "C" pa_status pa_prefill_varlen_packed(void* out, const void* q, const vo
     CUtensorMap map_q;
     if (!make_q_map(&map_q, q, num_heads, group, num_seqs, max_seqlen_q, dtype)) return PA_ERR_CUDA;
     p.q_rows = q_map_rows(num_seqs, max_seqlen_q);
-    return launch_prefill<true>(p, dtype, map_k, map_v, map_q, stream);
+    return launch_prefill<true, false>(p, dtype, map_k, map_v, map_q, stream);
 }

@@ -67,3 +67,15 @@ def test_reference_against_a_dense_softmax():
     want = torch.nn.functional.scaled_dot_product_attention(q.double().transpose(0, 1), K, V, t <= p, scale=0.125)
     assert torch.allclose(full, want.transpose(0, 1), atol=1e-12)
     assert R.seen_blocks(45, 44, 9, 3, 16).tolist() == [True, False, True]
+
+
+def test_prefill_window_rejects_bad_arguments_before_launch(lib):
+    def call(c=None, H=4, dt=pk.PA_F16, window=8, sinks=2, scale=0.1, n=2, max_q=8, bt=FAKE):
+        return lib.pa_prefill_varlen_window(FAKE, FAKE, dt, C.byref(c or cache()), bt, 4, FAKE, FAKE, n, max_q, 64, H,
+                                            scale, window, sinks, None, None)
+    assert call(window=0) == 1 and call(window=-5) == 1 and call(sinks=-1) == 1
+    assert call(scale=0.0) == 1 and call(scale=-0.1) == 1 and call(scale=math.nan) == 1 and call(scale=math.inf) == 1
+    assert call(H=3) == 1 and call(bt=None) == 1
+    assert call(dt=pk.PA_BF16) == 2 and call(c=cache(head_size=64)) == 2 and call(c=cache(block_size=8)) == 2
+    assert call(c=cache(kv_dtype=pk.PA_FP8_E4M3)) == 2
+    assert call(n=0) == 0 and call(max_q=0) == 0
