@@ -314,7 +314,8 @@ pa_status pa_decode_static_ws(void* out, const void* q, pa_dtype q_dtype, const 
  * pa_pool_release_window), and what the blocks hold at positions that are not
  * seen (NaN included) takes no part.
  * partition_size counts the tokens of the blocks read (the sinks' whole blocks,
- * then the window's); 0 chooses one.  workspace: pa_decode_window_workspace_size
+ * then the window's); 0 cuts them into equal parts that fill the GPU, of 128
+ * tokens or more.  workspace: pa_decode_window_workspace_size
  * (...) bytes with the same arguments.  Everything else as pa_decode.
  * ------------------------------------------------------------------------- */
 size_t pa_decode_window_workspace_size(int32_t num_seqs, int32_t num_heads, int32_t head_size, int32_t max_seq_len,

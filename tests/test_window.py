@@ -28,11 +28,14 @@ def cache(**kw):
 
 def test_decode_window_workspace(lib):
     size = pk.pa_decode_window_workspace_size
-    # the sinks' block, the window's and the rest of its first: 16 + 480 + 15 tokens fit one partition of 512
-    assert size(4, 8, 128, 100000, 16, 480, 4) == 0
+    # the sinks' block, the window's and the rest of its first: 16 + 481 + 15 tokens fit one partition of 512
+    assert size(4, 8, 128, 100000, 16, 481, 4, 512) == 0
     rows = 4 * 8 * 2
-    assert size(4, 8, 128, 100000, 16, 500, 4) >= rows * 129 * 4
-    assert size(4, 8, 128, 100000, 16, 500, 4) < pk.pa_decode_workspace_size(4, 8, 128, 100000, 16)
+    assert size(4, 8, 128, 100000, 16, 482, 4, 512) >= rows * 129 * 4
+    # automatic: parts of 128 tokens or more
+    assert size(4, 8, 128, 100000, 16, 97, 4) == 0
+    assert rows * 129 * 4 <= size(4, 8, 128, 100000, 16, 98, 4) < size(4, 8, 128, 100000, 16, 2000, 4)
+    assert size(4, 8, 128, 100000, 16, 2000, 4) < pk.pa_decode_workspace_size(4, 8, 128, 100000, 16)
     assert size(4, 8, 128, 300, 16, MAX, MAX, 128) == pk.pa_decode_workspace_size(4, 8, 128, 300, 16, 128)
     assert size(4, 8, 128, 300, 16, 0, 4) == 0 and size(4, 8, 128, 300, 16, 8, -1) == 0
 
