@@ -95,6 +95,10 @@ struct DecodeParams {
     // and the first `sinks`
     int32_t window;
     int32_t sinks;
+    // windowed decode: the grid holds an item for every (sequence, partition, KV
+    // head) that max_parts allows, so block i takes item i and no work list is
+    // built (its sort takes 2.3 us, a third of a small batch's decode)
+    int32_t one_round;
     // test hook (pa_decode_test_wait_timeout; 0 on every other path): the
     // producer warp issues no copy at all, so every consumer wait runs out
     // with nothing in flight, reports PA_ERR_TIMEOUT and the block returns
@@ -420,9 +424,17 @@ __device__ __forceinline__ Item decode_item(const DecodeParams& p, const int32_t
     Item it;
     const int sp = i / p.num_kv_heads;
     it.kvh = i - sp * p.num_kv_heads;
-    const int F = prefix[p.num_seqs];
+    const int F = WIN && p.one_round ? 0 : prefix[p.num_seqs];
     int L;
-    if (sp < F) {
+    if (WIN && p.one_round) {
+        // (a part past the sequence's last gives part >= nparts: no item)
+        it.b = sp / p.max_parts;
+        it.part = sp - it.b * p.max_parts;
+        L = checked_len<WIN>(p, it.b);
+        it.L = max(L, 0);
+        it.s0 = 0;
+        it.nparts = parts_of(it.L, p.partition);
+    } else if (sp < F) {
         int lo = 0, hi = p.num_seqs - 1;  // largest b with prefix[b] <= sp
         while (lo < hi) {
             int mid = (lo + hi + 1) >> 1;
@@ -1093,9 +1105,18 @@ paged_decode_kernel(const DecodeParams p) {
     }
     // merge area doubles as scan scratch before the first item
     int32_t* order = reinterpret_cast<int32_t*>(smem_raw + L.order);
-    build_schedule<WIN>(p, prefix, order, reinterpret_cast<int32_t*>(merge), smem_raw + L.keys,
-                   reinterpret_cast<int32_t*>(smem_raw + L.hist));
-    const int n_items = (prefix[p.num_seqs] + p.num_seqs) * p.num_kv_heads;
+    int n_items;
+    if (WIN && p.one_round) {
+        __syncthreads();  // (the barriers are set up)
+        const Item it = decode_item<WIN>(p, prefix, order, blockIdx.x);
+        if (it.part >= it.nparts) return;
+        if (it.part == 0 && threadIdx.x == 0 && true_len(p, it.b) < 0) report(p.status, PA_ERR_INVALID_ARG);
+        n_items = gridDim.x;
+    } else {
+        build_schedule<WIN>(p, prefix, order, reinterpret_cast<int32_t*>(merge), smem_raw + L.keys,
+                            reinterpret_cast<int32_t*>(smem_raw + L.hist));
+        n_items = (prefix[p.num_seqs] + p.num_seqs) * p.num_kv_heads;
+    }
 
     if (warp == C::NCW) {
         // ------------------------------ producer ------------------------------

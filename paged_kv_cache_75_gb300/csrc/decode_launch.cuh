@@ -44,6 +44,7 @@ pa_status launch_decode_t(DecodeParams p, cudaStream_t stream) {
     const int64_t cap = static_cast<int64_t>(sms) * per_sm;
     const int grid = static_cast<int>(max_items < cap ? max_items : cap);
     if (grid <= 0) return PA_OK;
+    p.one_round = mode == kWindow && max_items <= cap ? 1 : 0;
     if (launch_pdl(kern, grid, C::THREADS, smem, stream, p) != cudaSuccess) return PA_ERR_CUDA;
     if (p.max_parts > 1) {
         // group mode: the merge runs over the batch's members

@@ -495,20 +495,27 @@ __device__ __forceinline__ Work work_item(const ParamsOf<WIN>& p, const int32_t*
     return w;
 }
 
-// scores of keys that are not seen: those from vis on, and (WIN) [hid0, hid1)
+// bits [0, n)
+__device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull; }
+
+// Scores of keys that are not seen: those from vis on and (WIN) [hid0, hid1).
+// (WIN: a bit test a score, whatever the two ranges.)
 template <bool WIN>
 __device__ __forceinline__ void hide_keys(float (&e)[64], int vis, int hid0, int hid1) {
-    if (vis < 64) {
+    if constexpr (WIN) {
+        const uint64_t seen = low_bits(vis) & ~(low_bits(hid1) & ~low_bits(hid0));
+        if (seen != ~0ull) {
+            const uint32_t s0 = static_cast<uint32_t>(seen), s1 = static_cast<uint32_t>(seen >> 32);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                if (!(s0 & (1u << i))) e[i] = -INFINITY;
+                if (!(s1 & (1u << i))) e[32 + i] = -INFINITY;
+            }
+        }
+    } else if (vis < 64) {
 #pragma unroll
         for (int i = 0; i < 64; ++i)
             if (i >= vis) e[i] = -INFINITY;
-    }
-    if constexpr (WIN) {
-        if (hid0 < hid1) {
-#pragma unroll
-            for (int i = 0; i < 64; ++i)
-                if (i >= hid0 && i < hid1) e[i] = -INFINITY;
-        }
     }
 }
 
@@ -620,7 +627,10 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
     }
     // ---- work order of the query tiles ----
     const int32_t* order = nullptr;
-    if (p.order_cap > 0 && prefix[B] <= p.order_cap) {
+    // (window: no more items than blocks need no order; sorting them took 1.3 us
+    // of a small batch's 11)
+    if (p.order_cap > 0 && prefix[B] <= p.order_cap &&
+        (!WIN || static_cast<int64_t>(prefix[B]) * p.num_kv_heads > gridDim.x)) {
         int32_t* ord = prefix + B + 1;
         build_tile_order<WIN>(p, prefix, prefix[B], ord, ord + p.order_cap);
         order = ord;
@@ -1045,7 +1055,10 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
                 float e[64];
                 float sum = 0.f;
                 bool over = false;
-                if (ok) {
+                // (window: an item's first tile has no reference, straight to the
+                // true maximum)
+                const bool first = WIN && t == 0;
+                if (ok && !first) {
                     tc_fence_after();
                     tmem_ld64(sbuf + b * kBN, e);
                     hide_keys<WIN>(e, vis, hid0, hid1);
@@ -1079,10 +1092,13 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
                         over = !(sum < kSafe);  // also catches inf and NaN
                     }
                 }
-                const bool any = bar_red_or(2, 256, over);
-                if (snapshot()) {
-                    stop = true;
-                    break;
+                bool any = true;
+                if (!first) {
+                    any = bar_red_or(2, 256, over);
+                    if (snapshot()) {
+                        stop = true;
+                        break;
+                    }
                 }
                 if (any) {
                     // slow path (all 256 threads): the tile's true row max over both
