@@ -548,6 +548,17 @@ pa_status pa_slot_mapping(const int32_t* block_table, int32_t num_seqs, int32_t 
  * pa_pool_block_table: host int32 [n][max_blocks] rows, -1 padded, and host
  *   int32 lens_out[n] (nullable).  A sequence with more blocks than
  *   max_blocks gives PA_ERR_INVALID_ARG.
+ * pa_pool_release_window(seq, window, num_sinks): gives back the blocks that no
+ *   query of the sequence from position len - 1 on sees with that window and
+ *   that many sinks (pa_decode_window, pa_prefill_varlen_window): those wholly
+ *   past the first num_sinks positions and wholly before position len - window.
+ *   Call it once the queries of the tokens appended last are the only ones left
+ *   to attend (a prefill's chunk of n tokens: with window + n - 1).  Each block's
+ *   reference count - 1, in logical order, a block reaching 0 goes to the tail of the
+ *   free list; the sequence's table holds -1 there from then on (a fork takes the
+ *   holes over; pa_decode and the other unwindowed calls report them as
+ *   PA_ERR_BAD_BLOCK).  *n_released_out (nullable): how many.  window >= 1,
+ *   num_sinks >= 0.
  * Sequence ids are arbitrary int64 keys; an unknown id gives
  * PA_ERR_INVALID_ARG.
  * ------------------------------------------------------------------------- */
@@ -559,6 +570,8 @@ pa_status pa_pool_append(void* pool, int64_t seq_id, int32_t n_tokens, int64_t* 
                          int32_t* cow_pairs_out, int32_t* n_cow_out);
 pa_status pa_pool_fork(void* pool, int64_t parent, int64_t child);
 pa_status pa_pool_free_seq(void* pool, int64_t seq_id);
+pa_status pa_pool_release_window(void* pool, int64_t seq_id, int32_t window, int32_t num_sinks,
+                                 int32_t* n_released_out);
 pa_status pa_pool_block_table(void* pool, const int64_t* seq_ids, int32_t n, int32_t max_blocks,
                               int32_t* table_out, int32_t* lens_out);
 int64_t pa_pool_num_free(void* pool);

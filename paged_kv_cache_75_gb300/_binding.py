@@ -72,6 +72,7 @@ def library():
             "pa_pool_append": ([vp, i64, i32, vp, vp, vp], C.c_int),
             "pa_pool_fork": ([vp, i64, i64], C.c_int),
             "pa_pool_free_seq": ([vp, i64], C.c_int),
+            "pa_pool_release_window": ([vp, i64, i32, i32, C.POINTER(i32)], C.c_int),
             "pa_pool_block_table": ([vp, vp, i32, i32, vp, vp], C.c_int),
             "pa_pool_num_free": ([vp], i64),
             "pa_pool_ref_count": ([vp, i64], i32),
@@ -728,6 +729,14 @@ class BlockPool:
 
     def free_seq(self, seq_id: int):
         _check(library().pa_pool_free_seq(self._h, seq_id), "pa_pool_free_seq")
+
+    def release_window(self, seq_id: int, window: int, num_sinks: int = 0) -> int:
+        """Gives back the blocks that no query from the sequence's last position
+        on sees; returns how many."""
+        n = C.c_int32(0)
+        _check(library().pa_pool_release_window(self._h, seq_id, window, num_sinks, C.byref(n)),
+               "pa_pool_release_window")
+        return n.value
 
     def block_table(self, seq_ids, max_blocks: int):
         n = len(seq_ids)

@@ -29,8 +29,9 @@
 namespace {
 
 struct Sequence {
-    std::vector<int32_t> blocks;  // logical index -> physical id
+    std::vector<int32_t> blocks;  // logical index -> physical id, -1 once released (pa_pool_release_window)
     int64_t length = 0;           // tokens held
+    int64_t released_from = 0, released_to = 0;  // every block of [from, to) is released
 };
 
 struct Pool {
@@ -135,7 +136,8 @@ pa_status pa_pool_fork(void* pool, int64_t parent, int64_t child) {
     auto it = p->seqs.find(parent);
     if (it == p->seqs.end()) return PA_ERR_INVALID_ARG;
     Sequence copy = it->second;
-    for (int32_t b : copy.blocks) p->ref[b] += 1;
+    for (int32_t b : copy.blocks)
+        if (b >= 0) p->ref[b] += 1;
     p->seqs.emplace(child, std::move(copy));
     return PA_OK;
 }
@@ -146,10 +148,53 @@ pa_status pa_pool_free_seq(void* pool, int64_t seq_id) {
     auto it = p->seqs.find(seq_id);
     if (it == p->seqs.end()) return PA_ERR_INVALID_ARG;
     for (int32_t b : it->second.blocks) {
+        if (b < 0) continue;
         p->ref[b] -= 1;
         if (p->ref[b] == 0) p->free_list.push_back(b);
     }
     p->seqs.erase(it);
+    return PA_OK;
+}
+
+pa_status pa_pool_release_window(void* pool, int64_t seq_id, int32_t window, int32_t num_sinks,
+                                 int32_t* n_released_out) {
+    Pool* p = as_pool(pool);
+    if (p == nullptr || window <= 0 || num_sinks < 0) return PA_ERR_INVALID_ARG;
+    auto it = p->seqs.find(seq_id);
+    if (it == p->seqs.end()) return PA_ERR_INVALID_ARG;
+    Sequence& s = it->second;
+    const int64_t bs = p->block_size;
+    // blocks wholly past the sinks and wholly before what the query at position
+    // length - 1 sees (later queries see no more of them); the last block stays:
+    // it holds that query's own position
+    const int64_t first = (static_cast<int64_t>(num_sinks) + bs - 1) / bs;
+    const int64_t lo = s.length - window;
+    const int64_t end = lo > 0 ? lo / bs : 0;
+    int32_t n = 0;
+    for (int64_t j = first; j < end; ++j) {
+        // (what earlier calls released: a step looks at its new blocks alone)
+        if (j >= s.released_from && j < s.released_to) j = s.released_to;
+        if (j >= end) break;
+        const int32_t b = s.blocks[j];
+        if (b < 0) continue;
+        if (p->ref[b] == 1) {
+            try {
+                p->free_list.push_back(b);
+            } catch (const std::bad_alloc&) {
+                if (n_released_out) *n_released_out = n;
+                return PA_ERR_OOM;  // the blocks so far are released, the others as they were
+            }
+        }
+        p->ref[b] -= 1;
+        s.blocks[j] = -1;
+        ++n;
+    }
+    if (first < end) {
+        const bool joins = s.released_from < s.released_to && first <= s.released_to && s.released_from <= end;
+        s.released_from = joins && s.released_from < first ? s.released_from : first;
+        s.released_to = joins && s.released_to > end ? s.released_to : end;
+    }
+    if (n_released_out) *n_released_out = n;
     return PA_OK;
 }
 
