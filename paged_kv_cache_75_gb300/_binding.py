@@ -130,21 +130,12 @@ def _stream(t: torch.Tensor):
     return C.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
 
 
-class _Here:
-    def __enter__(self):
-        pass
-
-    def __exit__(self, *a):
-        pass
-
-
-_here = _Here()
-
-
-def _on(device):
-    """The device of the call's tensors, as a context (nothing to do when it is
-    the current one already)."""
-    return _here if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+def _call(fn, index, *args):
+    """fn(*args, stream) on the device of the call's tensors and its current stream."""
+    if index == torch._C._cuda_getDevice():
+        return fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    with torch.cuda.device(index):
+        return fn(*args, torch._C._cuda_getCurrentRawStream(index))
 
 
 def _need(t, name, dtype=None, cuda=True):
@@ -221,7 +212,7 @@ def pa_kv_cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slot_map
 ROPE_KINDS = ("none", "linear", "ntk", "yarn", "banded", "given")
 
 
-@dataclass
+@dataclass(frozen=True)
 class RopeFrequencies:
     """Frequencies of a rotation: theta (radians per position, host float64
     [rotary_dim/2]), turns (the same as turns per position in units of 2^-64,
@@ -264,11 +255,12 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "non
     return RopeFrequencies(th, torch.from_numpy(turns.view(np.int64)).to(device), float(out_factor.value))
 
 
-@dataclass
+@dataclass(frozen=True)
 class QKTransform:
     """What pa_qk_norm_rope does to each head's row: the norm (q_weight,
     k_weight: float32 [head_size]; None: not normed), then the rotation (rope;
-    None: none), in pairs (i, i + rotary_dim/2) or, interleaved, (2i, 2i+1)."""
+    None: none), in pairs (i, i + rotary_dim/2) or, interleaved, (2i, 2i+1).
+    A program makes it once; what the tensors hold is read by every call."""
     rope: Optional[RopeFrequencies] = None
     interleaved: bool = False
     q_weight: Optional[torch.Tensor] = None
@@ -276,40 +268,42 @@ class QKTransform:
     eps: float = 1e-6
 
     def __post_init__(self):
+        r = self.rope
+        given = []  # (tensor, field of the C struct)
         for name, w in (("q_weight", self.q_weight), ("k_weight", self.k_weight)):
             if w is not None:
                 _need(w, name, torch.float32)
-        if self.rope is not None:
-            _need(self.rope.turns, "rope.turns", torch.int64)
-
-    def c_struct(self, head_size: int, device) -> _QKTransform:
-        r, qw, kw = self.rope, self.q_weight, self.k_weight
-        c = _QKTransform(eps=self.eps, rope_factor=1.0, interleaved=1 if self.interleaved else 0)
-        if qw is not None:
-            c.q_weight = _on_device(qw, "q_weight", head_size, device)
-        if kw is not None:
-            c.k_weight = _on_device(kw, "k_weight", head_size, device)
+                if w.dim() != 1:
+                    raise ValueError("%s must be [head_size]" % name)
+                given.append((w, name))
         if r is not None:
-            n = r.turns.shape[0]
-            c.turns = _on_device(r.turns, "rope.turns", n, device)
-            c.rope_factor = r.factor
-            c.rotary_dim = 2 * n
+            _need(r.turns, "rope.turns", torch.int64)
+            given.append((r.turns, "turns"))
+        if len({t.get_device() for t, _ in given}) > 1:
+            raise ValueError("the transform's tensors must be on one device")
+        if len({t.shape[0] for t, f in given if f != "turns"}) > 1:
+            raise ValueError("q_weight and k_weight must have one head size")
+        object.__setattr__(self, "_given", given)
+        object.__setattr__(self, "_c", _QKTransform(eps=float(self.eps), interleaved=1 if self.interleaved else 0,
+                                                    rope_factor=1.0 if r is None else float(r.factor),
+                                                    rotary_dim=0 if r is None else r.rotary_dim))
+
+    def c_struct(self, head_size: int, index: int) -> _QKTransform:
+        c = self._c
+        for t, field in self._given:
+            if t.get_device() != index or (field != "turns" and t.shape[0] != head_size):
+                raise ValueError("the transform's tensors must be on the rows' device, the weights of the rows' head size")
+            setattr(c, field, t.data_ptr())
         return c
 
 
-def _on_device(t, name, n, device):
-    if t.shape != (n,) or t.device != device:
-        raise ValueError("%s must have %d entries on the rows' device" % (name, n))
-    return t.data_ptr()
-
-
-def _rows(t, name, shape, dtype, device):
+def _rows(t, name, shape, dtype, index):
     """Checks [T, heads, head_size] rows whose tokens may be strided; returns
     the token stride."""
-    if t.shape != shape or t.dtype != dtype or t.device != device:
-        raise ValueError("%s must be %s %s on %s" % (name, dtype, tuple(shape), device))
-    T, n, D = shape
+    if t.shape != shape or t.dtype != dtype or t.get_device() != index:
+        raise ValueError("%s must be %s %s on device %d" % (name, dtype, tuple(shape), index))
     st, sh, sd = t.stride()
+    T, n, D = shape
     if sd != 1 or (sh != D and n > 1):
         raise ValueError("the heads of a token of %s must be contiguous" % name)
     return st if T > 1 else max(st, n * D)  # (a single token's stride says nothing)
@@ -321,24 +315,51 @@ def _rows_of(t, name):
     return t.shape
 
 
-def _token_index(t, name, tokens, device):
+def _token_index(t, name, tokens, index):
     if t.dtype != torch.int64:
         raise TypeError("%s must be torch.int64" % name)
-    if t.shape != (tokens,) or t.device != device or not t.is_contiguous():
+    if t.shape != (tokens,) or t.get_device() != index or not t.is_contiguous():
         raise ValueError("%s must be contiguous int64 [tokens] on the queries' device" % name)
     return t.data_ptr()
 
 
-def _status_ptr(t, device):
+def _ints(t, name, shape, index):
+    """A contiguous int32 tensor of that shape (None: any size there) on the device; its address."""
+    if t.dtype != torch.int32:
+        raise TypeError("%s must be torch.int32" % name)
+    if len(t.shape) != len(shape) or any(n is not None and m != n for m, n in zip(t.shape, shape)) or \
+            t.get_device() != index or not t.is_contiguous():
+        raise ValueError("%s must be contiguous int32 of shape %s on the queries' device" % (name, shape))
+    return t.data_ptr()
+
+
+def _status_ptr(t, index):
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.device != device:
+    if t.dtype != torch.int32 or t.get_device() != index:
         raise ValueError("dev_status must be int32 on the queries' device")
     return t.data_ptr()
 
 
-def _raw_stream(device):
-    return torch._C._cuda_getCurrentRawStream(device.index)
+def _scratch(t, index):
+    if t is None:
+        return None, 0
+    if t.get_device() != index or not t.is_contiguous():
+        raise ValueError("workspace must be contiguous on the queries' device")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _queries(q, out, cache):
+    """Checks contiguous q and out [rows, num_heads, head_size] beside the cache;
+    returns the shape, the type's code and the device."""
+    shape = _rows_of(q, "q")
+    index = q.get_device()
+    if not q.is_contiguous() or not out.is_contiguous() or out.shape != shape or out.dtype != q.dtype or \
+            out.get_device() != index:
+        raise ValueError("q and out must be contiguous and of one shape, type and device")
+    if cache.k_cache.shape[3] != shape[2] or cache.k_cache.get_device() != index:
+        raise ValueError("the cache must have the queries' head size and device")
+    return shape, torch_dtype_code(q.dtype), index
 
 
 def pa_qk_norm_rope(q_out: torch.Tensor, k_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
@@ -349,18 +370,15 @@ def pa_qk_norm_rope(q_out: torch.Tensor, k_out: torch.Tensor, q: torch.Tensor, k
     positions: int64 [T]."""
     shape, kshape = _rows_of(q, "q"), _rows_of(k, "k")
     T, H, D = shape
-    dt, dev = q.dtype, q.device
+    dt, dev = q.dtype, q.get_device()
     if kshape[0] != T or kshape[2] != D:
         raise ValueError("k must have the queries' tokens and head size")
     qs, ks = _rows(q, "q", shape, dt, dev), _rows(k, "k", kshape, dt, dev)
     qos, kos = _rows(q_out, "q_out", shape, dt, dev), _rows(k_out, "k_out", kshape, dt, dev)
     pos = None if positions is None else _token_index(positions, "positions", T, dev)
-    tr = transform.c_struct(D, dev)
-    with _on(dev):
-        st = library().pa_qk_norm_rope(q_out.data_ptr(), k_out.data_ptr(), q.data_ptr(), k.data_ptr(),
-                                       torch_dtype_code(dt), T, H, kshape[1], D, qs, ks, qos, kos, pos, tr,
-                                       _raw_stream(dev))
-    _check(st, "pa_qk_norm_rope")
+    _check(_call(library().pa_qk_norm_rope, dev, q_out.data_ptr(), k_out.data_ptr(), q.data_ptr(), k.data_ptr(),
+                 torch_dtype_code(dt), T, H, kshape[1], D, qs, ks, qos, kos, pos, transform.c_struct(D, dev)),
+           "pa_qk_norm_rope")
 
 
 def pa_qk_norm_rope_write(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: KVCache,
@@ -370,21 +388,18 @@ def pa_qk_norm_rope_write(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
     slot_mapping's (int64 [T], < 0 skips) slots of the cache."""
     shape = _rows_of(q, "q")
     T, H, D = shape
-    dt, dev = q.dtype, q.device
+    dt, dev = q.dtype, q.get_device()
     cs = cache.c_struct()
-    if D != cs.head_size or cache.k_cache.device != dev:
+    if D != cs.head_size or cache.k_cache.get_device() != dev:
         raise ValueError("the cache must have the queries' head size and device")
     kshape = (T, cs.num_kv_heads, D)
     qs, ks, vs = _rows(q, "q", shape, dt, dev), _rows(k, "k", kshape, dt, dev), _rows(v, "v", kshape, dt, dev)
     qos = _rows(q_out, "q_out", shape, dt, dev)
     pos = None if positions is None else _token_index(positions, "positions", T, dev)
-    slots = _token_index(slot_mapping, "slot_mapping", T, dev)
-    tr = transform.c_struct(D, dev)
-    with _on(dev):
-        st = library().pa_qk_norm_rope_write(q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                             torch_dtype_code(dt), cs, T, H, qs, ks, vs, qos, pos, slots, tr,
-                                             _status_ptr(dev_status, dev), _raw_stream(dev))
-    _check(st, "pa_qk_norm_rope_write")
+    _check(_call(library().pa_qk_norm_rope_write, dev, q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                 torch_dtype_code(dt), cs, T, H, qs, ks, vs, qos, pos,
+                 _token_index(slot_mapping, "slot_mapping", T, dev), transform.c_struct(D, dev),
+                 _status_ptr(dev_status, dev)), "pa_qk_norm_rope_write")
 
 
 def pa_copy_blocks(cache: KVCache, src_dst_pairs: torch.Tensor, dev_status: Optional[torch.Tensor] = None):
@@ -490,14 +505,8 @@ def pa_decode(out: torch.Tensor, q: torch.Tensor, cache: KVCache, block_table: t
 
 def pa_decode_window_workspace_size(num_seqs, num_heads, head_size, max_seq_len, block_size, window, num_sinks=0,
                                     partition_size=0) -> int:
-    return int(library().pa_decode_window_workspace_size(num_seqs, num_heads, head_size, max_seq_len, block_size,
-                                                         window, num_sinks, partition_size))
-
-
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError("%s must be on the queries' device" % name)
+    return int(library().pa_decode_window_workspace_size(num_seqs, num_heads, head_size, int(max_seq_len), block_size,
+                                                         int(window), int(num_sinks), int(partition_size)))
 
 
 def pa_decode_window(out: torch.Tensor, q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
@@ -507,27 +516,14 @@ def pa_decode_window(out: torch.Tensor, q: torch.Tensor, cache: KVCache, block_t
     """pa_decode where each query sees the last `window` tokens (its own
     included) and the first num_sinks; block-table entries of blocks that hold
     neither are not read."""
-    _need(q, "q")
-    _need(out, "out", q.dtype)
-    _need(block_table, "block_table", torch.int32)
-    _need(seq_lens, "seq_lens", torch.int32)
-    B, H, D = q.shape
-    dev = q.device
-    if out.shape != q.shape or block_table.dim() != 2 or block_table.shape[0] != B or seq_lens.shape != (B,) or \
-            D != cache.head_size:
-        raise ValueError("out must have q's shape, block_table [num_seqs, max_blocks], seq_lens [num_seqs], the cache "
-                         "q's head size")
-    _same_device(dev, out=out, cache=cache.k_cache, block_table=block_table, seq_lens=seq_lens, workspace=workspace)
-    if workspace is not None:
-        _need(workspace, "workspace")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    with _on(dev):
-        st = library().pa_decode_window(out.data_ptr(), q.data_ptr(), torch_dtype_code(q.dtype), cache.c_struct(),
-                                        block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), B,
-                                        int(max_seq_len), H, float(scale), int(window), int(num_sinks),
-                                        int(partition_size), None if workspace is None else workspace.data_ptr(),
-                                        ws_bytes, _status_ptr(dev_status, dev), _raw_stream(dev))
-    _check(st, "pa_decode_window")
+    (B, H, _), code, dev = _queries(q, out, cache)
+    table = _ints(block_table, "block_table", (B, None), dev)
+    lens = _ints(seq_lens, "seq_lens", (B,), dev)
+    ws, ws_bytes = _scratch(workspace, dev)
+    _check(_call(library().pa_decode_window, dev, out.data_ptr(), q.data_ptr(), code, cache.c_struct(), table,
+                 block_table.shape[1], lens, B, int(max_seq_len), H, float(scale), int(window), int(num_sinks),
+                 int(partition_size), ws, ws_bytes,
+                 _status_ptr(dev_status, dev)), "pa_decode_window")
 
 
 def pa_decode_test_wait_timeout(out: torch.Tensor, q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
@@ -658,27 +654,15 @@ def pa_prefill_varlen_window(out: torch.Tensor, q: torch.Tensor, cache: KVCache,
     """pa_prefill_varlen, causal, where a query at position x sees the keys of
     positions x - window + 1 .. x and the first num_sinks; block-table entries
     of blocks that no query sees are not read."""
-    _need(q, "q")
-    _need(out, "out", q.dtype)
-    _need(block_table, "block_table", torch.int32)
-    _need(cu_seq_lens_q, "cu_seq_lens_q", torch.int32)
-    _need(cu_seq_lens_k, "cu_seq_lens_k", torch.int32)
-    dev = q.device
+    (_, H, _), code, dev = _queries(q, out, cache)
     B = cu_seq_lens_q.shape[0] - 1
-    if q.dim() != 3 or out.shape != q.shape or block_table.dim() != 2 or block_table.shape[0] != B or \
-            cu_seq_lens_k.shape != cu_seq_lens_q.shape or q.shape[2] != cache.head_size:
-        raise ValueError("out must have q's shape [total_q, num_heads, head_size], block_table [num_seqs, max_blocks], "
-                         "cu_seq_lens_q and _k [num_seqs + 1], the cache q's head size")
-    _same_device(dev, out=out, cache=cache.k_cache, block_table=block_table, cu_seq_lens_q=cu_seq_lens_q,
-                 cu_seq_lens_k=cu_seq_lens_k)
-    with _on(dev):
-        st = library().pa_prefill_varlen_window(out.data_ptr(), q.data_ptr(), torch_dtype_code(q.dtype),
-                                                cache.c_struct(), block_table.data_ptr(), block_table.shape[1],
-                                                cu_seq_lens_q.data_ptr(), cu_seq_lens_k.data_ptr(), B,
-                                                int(max_seqlen_q), int(max_seqlen_k), q.shape[1], float(scale),
-                                                int(window), int(num_sinks), _status_ptr(dev_status, dev),
-                                                _raw_stream(dev))
-    _check(st, "pa_prefill_varlen_window")
+    cu_q = _ints(cu_seq_lens_q, "cu_seq_lens_q", (B + 1,), dev)
+    cu_k = _ints(cu_seq_lens_k, "cu_seq_lens_k", (B + 1,), dev)
+    table = _ints(block_table, "block_table", (B, None), dev)
+    _check(_call(library().pa_prefill_varlen_window, dev, out.data_ptr(), q.data_ptr(), code, cache.c_struct(), table,
+                 block_table.shape[1], cu_q, cu_k, B, int(max_seqlen_q), int(max_seqlen_k), H, float(scale), int(window),
+                 int(num_sinks),
+                 _status_ptr(dev_status, dev)), "pa_prefill_varlen_window")
 
 
 def pa_slot_mapping(block_table, block_size: int, seq_idx, pos):
