@@ -503,8 +503,8 @@ __device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0ull : n >
 template <bool WIN>
 __device__ __forceinline__ void hide_keys(float (&e)[64], int vis, int hid0, int hid1) {
     if constexpr (WIN) {
-        const uint64_t seen = low_bits(vis) & ~(low_bits(hid1) & ~low_bits(hid0));
-        if (seen != ~0ull) {
+        if (vis < 64 || hid0 < hid1) {
+            const uint64_t seen = low_bits(vis) & ~(low_bits(hid1) & ~low_bits(hid0));
             const uint32_t s0 = static_cast<uint32_t>(seen), s1 = static_cast<uint32_t>(seen >> 32);
 #pragma unroll
             for (int i = 0; i < 32; ++i) {

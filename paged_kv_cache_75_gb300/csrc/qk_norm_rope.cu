@@ -66,6 +66,7 @@ struct NormRopeParams {
     int64_t num_tokens;
     int64_t num_slots;
     float eps, rope_factor, k_scale, v_scale;
+    float k_inverse, v_inverse;  // 1 / scale where the scale is a power of two, else 0
     int32_t num_heads, num_kv_heads;
     int32_t rotary_dim, interleaved, block_size;
     // each warp takes tokens w, w + warps, ... for `rounds` rounds, then a run of
@@ -139,14 +140,18 @@ __device__ __forceinline__ uint64_t widen(uint32_t w) {
     return pair2(f.x, f.y);
 }
 
-// 8 values (packed pairs) -> 8 E4M3 codes: IEEE division, then one rounding with saturation
-__device__ __forceinline__ uint2 e4m3_8(const uint64_t* x, float scale) {
+// 8 values (packed pairs) -> 8 E4M3 codes: IEEE division, then one rounding with
+// saturation.  (By a power of two, x / scale and x * (1 / scale) are the same
+// number rounded once; 16 divisions a lane cost a batch of 256 tokens a
+// quarter of its 5.1 us.)
+__device__ __forceinline__ uint2 e4m3_8(const uint64_t* x, float scale, float inverse) {
     uint32_t c[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const float2 f = unpair2(x[j]);
-        c[j] = static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(
-            make_float2(__fdiv_rn(f.x, scale), __fdiv_rn(f.y, scale)), __NV_SATFINITE, __NV_E4M3));
+        float2 f = unpair2(x[j]);
+        if (inverse != 0.f) f = unpair2(mul2(x[j], pair2(inverse, inverse)));
+        else f = make_float2(__fdiv_rn(f.x, scale), __fdiv_rn(f.y, scale));
+        c[j] = static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3));
     }
     return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
@@ -422,8 +427,9 @@ __device__ __forceinline__ void do_steps(const NormRopeParams& p, Run<KVT, D>& u
         if (rows <= 0) continue;
         if constexpr (ES == 1) {
             const float scale = KIND == 2 ? p.v_scale : p.k_scale;
-            *reinterpret_cast<uint2*>(dst) = e4m3_8(y, scale);
-            *reinterpret_cast<uint2*>(dst + u.gap) = e4m3_8(y + 4, scale);
+            const float inverse = KIND == 2 ? p.v_inverse : p.k_inverse;
+            *reinterpret_cast<uint2*>(dst) = e4m3_8(y, scale, inverse);
+            *reinterpret_cast<uint2*>(dst + u.gap) = e4m3_8(y + 4, scale, inverse);
         } else {
             // (elements that nothing changed keep their bits)
             const bool vec = KIND == 0 ? p.qo_vec : KVT == kPacked ? p.ko_vec : true;
@@ -513,6 +519,12 @@ qk_norm_rope_kernel(const NormRopeParams p) {
         }
     }
     // (the run's last groups are empty: no copy is on its way)
+}
+
+// 1 / x where x is a power of two (and 1 / x a normal number), else 0
+float power_of_two_inverse(float x) {
+    int e;
+    return std::frexp(x, &e) == 0.5f && e >= -125 && e <= 126 ? 1.f / x : 0.f;
 }
 
 bool aligned16(const void* ptr, int64_t stride) {
@@ -657,6 +669,8 @@ extern "C" pa_status pa_qk_norm_rope_write(void* q_out, const void* q, const voi
     p.num_slots = cache->num_blocks * cache->block_size;
     p.k_scale = cache->k_scale;
     p.v_scale = cache->v_scale;
+    p.k_inverse = power_of_two_inverse(cache->k_scale);
+    p.v_inverse = power_of_two_inverse(cache->v_scale);
     return launch(p, dtype, fp8 ? PA_FP8_E4M3 : static_cast<int>(dtype), cache->head_size,
                   reinterpret_cast<cudaStream_t>(stream));
 }

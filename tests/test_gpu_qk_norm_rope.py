@@ -112,6 +112,26 @@ def test_write_to_the_cache(kv, D, H, Hkv, bs, T):
     assert torch.equal(got_k.view(bits)[keep], kc0.view(bits)[keep])
 
 
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("ks,vs", [(1.0, 1.0), (0.25, 4.0), (3.0, 0.7), (2.0 ** -126, 2.0 ** 126), (2.0 ** -20, 2.0 ** 127)])
+def test_e4m3_scales(dt, ks, vs):
+    """Scales that are powers of two and not, at the ends of the range: keys and values that nothing turns are stored
+    as pa_kv_cache_write stores them, bit for bit, saturated ones, subnormal ones and infinities among them."""
+    T, H, Hkv, D, bs = 50, 2, 2, 128, 16
+    x, pos, _, _ = make(T, H, Hkv, D, TYPES[dt], seed=3)
+    x[5, :, 3], x[6, :, 4], x[7] = float("inf"), float("-inf"), x[7] * 1000
+    x[8] = (x[8].float() * 2.0 ** -12).to(x.dtype)
+    xd = x.to(DEV)
+    q, k, v = xd[:, :H], xd[:, H:H + Hkv], xd[:, H + Hkv:]
+    zero = torch.zeros(4, Hkv, bs, D, device=DEV).to(torch.float8_e4m3fn)
+    a, b = pk.KVCache(zero.clone(), zero.clone(), ks, vs), pk.KVCache(zero.clone(), zero.clone(), ks, vs)
+    slots = torch.arange(T, device=DEV) + 5
+    pk.pa_qk_norm_rope_write(torch.empty_like(q.contiguous()), q, k, v, a, pos.to(DEV), slots, pk.QKTransform())
+    pk.pa_kv_cache_write(b, k, v, slots)
+    assert torch.equal(a.k_cache.view(torch.uint8), b.k_cache.view(torch.uint8))
+    assert torch.equal(a.v_cache.view(torch.uint8), b.v_cache.view(torch.uint8))
+
+
 def test_slots_past_the_cache_are_reported_and_skipped():
     T, H, Hkv, D, bs = 9, 4, 2, 128, 16
     x, pos, qw, kw = make(T, H, Hkv, D, torch.float16)
