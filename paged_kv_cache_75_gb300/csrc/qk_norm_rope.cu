@@ -207,12 +207,16 @@ struct Loader {
         if (left > 0) {
             const bool have = rows > 0;
             if (vec) {
-                const uint16_t* from = have ? src : p.q;
+                // (nothing is read for a row past the segment's, but its address has
+                // to be an aligned one, which q's need not be here)
+                const uint64_t nowhere = reinterpret_cast<uint64_t>(p.q) & ~uint64_t{15};
+                const uint64_t from = have ? reinterpret_cast<uint64_t>(src) : nowhere;
+                const uint64_t from1 = have ? reinterpret_cast<uint64_t>(src + gap) : nowhere;
                 const uint32_t n = have ? 16u : 0u;
                 asm volatile(
                     "cp.async.cg.shared.global [%0], [%1], 16, %3;\n\t"
                     "cp.async.cg.shared.global [%0 + 512], [%2], 16, %3;" ::"r"(smem_addr(slot)),
-                    "l"(reinterpret_cast<uint64_t>(from)), "l"(reinterpret_cast<uint64_t>(have ? src + gap : p.q)), "r"(n)
+                    "l"(from), "l"(from1), "r"(n)
                     : "memory");
             } else {
                 slot[0] = have ? load_odd8(src) : make_uint4(0u, 0u, 0u, 0u);
@@ -584,7 +588,9 @@ pa_status prepare(NormRopeParams& p, void* q_out, const void* q, const void* k, 
     if (q_stride < qrow || q_out_stride < qrow || k_stride < krow) return PA_ERR_INVALID_ARG;
     if (tr->rotary_dim < 0 || tr->rotary_dim > head_size) return PA_ERR_INVALID_ARG;
     if (tr->rotary_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
-    if (tr->rotary_dim > 0 && (tr->turns == nullptr || !std::isfinite(tr->rope_factor))) return PA_ERR_INVALID_ARG;
+    if (tr->rotary_dim > 0 && (tr->turns == nullptr || (reinterpret_cast<uintptr_t>(tr->turns) & 7u) ||
+                               !std::isfinite(tr->rope_factor)))
+        return PA_ERR_INVALID_ARG;
     if ((tr->q_weight != nullptr || tr->k_weight != nullptr) && !(tr->eps > 0.f && std::isfinite(tr->eps)))
         return PA_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(tr->q_weight) & 15u) || (reinterpret_cast<uintptr_t>(tr->k_weight) & 15u))

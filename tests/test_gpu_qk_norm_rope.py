@@ -188,6 +188,31 @@ def test_strides_and_alignments(offset, pad, D):
     assert torch.equal(cache.v_cache.permute(0, 2, 1, 3).reshape(32, Hkv, D)[3:3 + T], v)
 
 
+@pytest.mark.parametrize("odd", ["q", "k", "v", "q_out"])
+@pytest.mark.parametrize("H,Hkv", [(1, 1), (3, 3), (5, 2), (4, 4)])
+def test_one_tensor_unaligned_beside_aligned_ones(odd, H, Hkv):
+    T, D, bs = 9, 128, 16
+    x, pos, qw, kw = make(T, H, Hkv, D, torch.float16, seed=H)
+    tr = transform(64, False, qw, kw)
+
+    def place(src, name):
+        n = src.shape[1]
+        flat = torch.zeros(T * n * D + 8, dtype=src.dtype, device=DEV)
+        at = flat[1:1 + T * n * D] if odd == name else flat[:T * n * D]
+        return at.view(T, n, D).copy_(src)
+
+    q, k, v = place(x[:, :H], "q"), place(x[:, H:H + Hkv], "k"), place(x[:, H + Hkv:], "v")
+    qo = place(torch.zeros(T, H, D, dtype=x.dtype), "q_out")
+    kc = torch.zeros(2, Hkv, bs, D, dtype=x.dtype, device=DEV)
+    cache = pk.KVCache(kc, kc.clone())
+    pk.pa_qk_norm_rope_write(qo, q, k, v, cache, pos.to(DEV), torch.arange(T, device=DEV), tr)
+    ref, pair = reference(x[:, :H], pos, tr, qw)
+    rope_ref.check(qo.cpu(), ref, pair, x.dtype)
+    ref, pair = reference(x[:, H:H + Hkv], pos, tr, kw)
+    rope_ref.check(kc.cpu()[0, :, :T].transpose(0, 1), ref, pair, x.dtype)
+    assert torch.equal(cache.v_cache.cpu()[0, :, :T].transpose(0, 1), x[:, H + Hkv:])
+
+
 def test_in_place_equals_out_of_place():
     T, H, Hkv, D = 300, 32, 8, 128
     x, pos, qw, kw = make(T, H, Hkv, D, torch.bfloat16)

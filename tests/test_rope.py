@@ -97,7 +97,7 @@ def test_rope_rejects_bad_arguments_before_launch(lib):
     assert _rope(lib, ok, q=None) == 1 and _rope(lib, ok, pos=None) == 1 and _rope(lib, ok, k_out=None) == 1
     assert _rope(lib, transform(rotary_dim=24)) == 2
     assert _rope(lib, transform(rotary_dim=144)) == 1 and _rope(lib, transform(rotary_dim=-16)) == 1
-    assert _rope(lib, transform(turns=None)) == 1
+    assert _rope(lib, transform(turns=None)) == 1 and _rope(lib, transform(turns=FAKE + 4)) == 1
     assert _rope(lib, transform(rope_factor=math.inf)) == 1
     assert _rope(lib, transform(eps=0.0)) == 1 and _rope(lib, transform(eps=math.nan)) == 1
     assert _rope(lib, transform(q_weight=FAKE + 4)) == 1 and _rope(lib, transform(k_weight=FAKE + 8)) == 1
