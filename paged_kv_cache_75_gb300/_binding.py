@@ -297,10 +297,13 @@ class QKTransform:
         return c
 
 
+_I32, _I64 = torch.int32, torch.int64
+
+
 def _rows(t, name, shape, dtype, index):
     """Checks [T, heads, head_size] rows whose tokens may be strided; returns
     the token stride."""
-    if t.shape != shape or t.dtype != dtype or t.get_device() != index:
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
         raise ValueError("%s must be %s %s on device %d" % (name, dtype, tuple(shape), index))
     st, sh, sd = t.stride()
     T, n, D = shape
@@ -315,28 +318,31 @@ def _rows_of(t, name):
     return t.shape
 
 
-def _token_index(t, name, tokens, index):
-    if t.dtype != torch.int64:
-        raise TypeError("%s must be torch.int64" % name)
-    if t.shape != (tokens,) or t.get_device() != index or not t.is_contiguous():
-        raise ValueError("%s must be contiguous int64 [tokens] on the queries' device" % name)
+def _vector(t, name, dtype, n, index):
+    """The address of a contiguous [n] tensor of that type on the device."""
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s" % (name, dtype))
+    if t.shape != (n,) or t.get_device() != index or not t.is_contiguous():
+        raise ValueError("%s must be contiguous [%d] on the queries' device" % (name, n))
     return t.data_ptr()
 
 
-def _ints(t, name, shape, index):
-    """A contiguous int32 tensor of that shape (None: any size there) on the device; its address."""
-    if t.dtype != torch.int32:
-        raise TypeError("%s must be torch.int32" % name)
-    if len(t.shape) != len(shape) or any(n is not None and m != n for m, n in zip(t.shape, shape)) or \
-            t.get_device() != index or not t.is_contiguous():
-        raise ValueError("%s must be contiguous int32 of shape %s on the queries' device" % (name, shape))
-    return t.data_ptr()
+def _table(t, rows, index):
+    """The address and width of a block table [rows, max_blocks]."""
+    if t.dtype is not _I32:
+        raise TypeError("block_table must be torch.int32")
+    if t.dim() != 2 or t.get_device() != index or not t.is_contiguous():
+        raise ValueError("block_table must be contiguous [num_seqs, max_blocks] on the queries' device")
+    n, width = t.shape
+    if n != rows:
+        raise ValueError("block_table must have %d rows" % rows)
+    return t.data_ptr(), width
 
 
 def _status_ptr(t, index):
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.get_device() != index:
+    if t.dtype is not _I32 or t.get_device() != index:
         raise ValueError("dev_status must be int32 on the queries' device")
     return t.data_ptr()
 
@@ -349,17 +355,17 @@ def _scratch(t, index):
     return t.data_ptr(), t.numel() * t.element_size()
 
 
-def _queries(q, out, cache):
-    """Checks contiguous q and out [rows, num_heads, head_size] beside the cache;
-    returns the shape, the type's code and the device."""
+def _queries(q, out, cs, cache):
+    """Checks contiguous q and out [rows, num_heads, head_size] beside the cache
+    (its C struct cs); returns the rows, the heads, the type's code, the device."""
     shape = _rows_of(q, "q")
-    index = q.get_device()
-    if not q.is_contiguous() or not out.is_contiguous() or out.shape != shape or out.dtype != q.dtype or \
-            out.get_device() != index:
+    index, dtype = q.get_device(), q.dtype
+    if out.shape != shape or out.dtype is not dtype or out.get_device() != index or not q.is_contiguous() or \
+            not out.is_contiguous():
         raise ValueError("q and out must be contiguous and of one shape, type and device")
-    if cache.k_cache.shape[3] != shape[2] or cache.k_cache.get_device() != index:
+    if cs.head_size != shape[2] or cache.k_cache.get_device() != index:
         raise ValueError("the cache must have the queries' head size and device")
-    return shape, torch_dtype_code(q.dtype), index
+    return shape[0], shape[1], torch_dtype_code(dtype), index
 
 
 def pa_qk_norm_rope(q_out: torch.Tensor, k_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
@@ -375,7 +381,7 @@ def pa_qk_norm_rope(q_out: torch.Tensor, k_out: torch.Tensor, q: torch.Tensor, k
         raise ValueError("k must have the queries' tokens and head size")
     qs, ks = _rows(q, "q", shape, dt, dev), _rows(k, "k", kshape, dt, dev)
     qos, kos = _rows(q_out, "q_out", shape, dt, dev), _rows(k_out, "k_out", kshape, dt, dev)
-    pos = None if positions is None else _token_index(positions, "positions", T, dev)
+    pos = None if positions is None else _vector(positions, "positions", _I64, T, dev)
     _check(_call(library().pa_qk_norm_rope, dev, q_out.data_ptr(), k_out.data_ptr(), q.data_ptr(), k.data_ptr(),
                  torch_dtype_code(dt), T, H, kshape[1], D, qs, ks, qos, kos, pos, transform.c_struct(D, dev)),
            "pa_qk_norm_rope")
@@ -395,10 +401,10 @@ def pa_qk_norm_rope_write(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
     kshape = (T, cs.num_kv_heads, D)
     qs, ks, vs = _rows(q, "q", shape, dt, dev), _rows(k, "k", kshape, dt, dev), _rows(v, "v", kshape, dt, dev)
     qos = _rows(q_out, "q_out", shape, dt, dev)
-    pos = None if positions is None else _token_index(positions, "positions", T, dev)
+    pos = None if positions is None else _vector(positions, "positions", _I64, T, dev)
     _check(_call(library().pa_qk_norm_rope_write, dev, q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
                  torch_dtype_code(dt), cs, T, H, qs, ks, vs, qos, pos,
-                 _token_index(slot_mapping, "slot_mapping", T, dev), transform.c_struct(D, dev),
+                 _vector(slot_mapping, "slot_mapping", _I64, T, dev), transform.c_struct(D, dev),
                  _status_ptr(dev_status, dev)), "pa_qk_norm_rope_write")
 
 
@@ -516,13 +522,13 @@ def pa_decode_window(out: torch.Tensor, q: torch.Tensor, cache: KVCache, block_t
     """pa_decode where each query sees the last `window` tokens (its own
     included) and the first num_sinks; block-table entries of blocks that hold
     neither are not read."""
-    (B, H, _), code, dev = _queries(q, out, cache)
-    table = _ints(block_table, "block_table", (B, None), dev)
-    lens = _ints(seq_lens, "seq_lens", (B,), dev)
+    cs = cache.c_struct()
+    B, H, code, dev = _queries(q, out, cs, cache)
+    table, width = _table(block_table, B, dev)
+    lens = _vector(seq_lens, "seq_lens", _I32, B, dev)
     ws, ws_bytes = _scratch(workspace, dev)
-    _check(_call(library().pa_decode_window, dev, out.data_ptr(), q.data_ptr(), code, cache.c_struct(), table,
-                 block_table.shape[1], lens, B, int(max_seq_len), H, float(scale), int(window), int(num_sinks),
-                 int(partition_size), ws, ws_bytes,
+    _check(_call(library().pa_decode_window, dev, out.data_ptr(), q.data_ptr(), code, cs, table, width, lens, B,
+                 int(max_seq_len), H, float(scale), int(window), int(num_sinks), int(partition_size), ws, ws_bytes,
                  _status_ptr(dev_status, dev)), "pa_decode_window")
 
 
@@ -654,14 +660,14 @@ def pa_prefill_varlen_window(out: torch.Tensor, q: torch.Tensor, cache: KVCache,
     """pa_prefill_varlen, causal, where a query at position x sees the keys of
     positions x - window + 1 .. x and the first num_sinks; block-table entries
     of blocks that no query sees are not read."""
-    (_, H, _), code, dev = _queries(q, out, cache)
+    cs = cache.c_struct()
+    _, H, code, dev = _queries(q, out, cs, cache)
     B = cu_seq_lens_q.shape[0] - 1
-    cu_q = _ints(cu_seq_lens_q, "cu_seq_lens_q", (B + 1,), dev)
-    cu_k = _ints(cu_seq_lens_k, "cu_seq_lens_k", (B + 1,), dev)
-    table = _ints(block_table, "block_table", (B, None), dev)
-    _check(_call(library().pa_prefill_varlen_window, dev, out.data_ptr(), q.data_ptr(), code, cache.c_struct(), table,
-                 block_table.shape[1], cu_q, cu_k, B, int(max_seqlen_q), int(max_seqlen_k), H, float(scale), int(window),
-                 int(num_sinks),
+    cu_q = _vector(cu_seq_lens_q, "cu_seq_lens_q", _I32, B + 1, dev)
+    cu_k = _vector(cu_seq_lens_k, "cu_seq_lens_k", _I32, B + 1, dev)
+    table, width = _table(block_table, B, dev)
+    _check(_call(library().pa_prefill_varlen_window, dev, out.data_ptr(), q.data_ptr(), code, cs, table, width, cu_q, cu_k,
+                 B, int(max_seqlen_q), int(max_seqlen_k), H, float(scale), int(window), int(num_sinks),
                  _status_ptr(dev_status, dev)), "pa_prefill_varlen_window")
 
 
