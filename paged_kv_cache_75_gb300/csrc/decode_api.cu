@@ -83,17 +83,18 @@ int window_partition(int64_t num_seqs, int num_kv_heads, int tokens, int block_s
     const int most = window_most_parts(num_seqs, tokens);
     int best = 0;
     double best_t = 0.0;
-    if (c <= 0.0) return (tokens + block_size - 1) / block_size * block_size;
     for (int n = 1; n <= most; n += n < 16 ? 1 : n / 8) {
-        int part = ((tokens + n - 1) / n + block_size - 1) / block_size * block_size;
+        int64_t part = ((static_cast<int64_t>(tokens) + n - 1) / n + block_size - 1) / block_size * block_size;
         if (part < block_size) part = block_size;
+        if (part > INT32_MAX / block_size * block_size) part = INT32_MAX / block_size * block_size;
+        if (c <= 0.0) return static_cast<int>(part);
         const double bytes = static_cast<double>(part) * token_bytes, items = pairs * n;
         const double full = std::floor(items / c), rest = items - full * c;
         double t = full * (c * bytes / memory + item) + (n > 1 ? merge : 0.0);
         if (rest > 0.0) t += std::fmax(bytes / block, rest * bytes / memory) + item;
         if (best == 0 || t <= best_t * 1.02) {
             if (best == 0 || t < best_t) best_t = t;
-            best = part;
+            best = static_cast<int>(part);
         }
     }
     return best;
