@@ -130,12 +130,26 @@ def _stream(t: torch.Tensor):
     return C.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
 
 
-def _call(fn, index, *args):
-    """fn(*args, stream) on the device of the call's tensors and its current stream."""
-    if index == torch._C._cuda_getDevice():
-        return fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    with torch.cuda.device(index):
-        return fn(*args, torch._C._cuda_getCurrentRawStream(index))
+_native_mod = None
+
+
+def _native():
+    """The CPython module that checks and marshals the calls of a decode step,
+    with the library's functions; raises if it has not been built."""
+    global _native_mod
+    if _native_mod is None:
+        try:
+            from . import _native as m
+        except ImportError as e:
+            raise RuntimeError("_native.so is missing: run __graft_entry__.build() "
+                               "(or python -m paged_kv_cache_75_gb300.build)") from e
+        L = library()
+        m.setup(torch.float16, torch.bfloat16, torch.float8_e4m3fn, torch.int32, torch.int64, torch.float32,
+                torch._C._cuda_getDevice, torch._C._cuda_setDevice, torch._C._cuda_getCurrentRawStream,
+                *[C.cast(f, C.c_void_p).value for f in (L.pa_qk_norm_rope, L.pa_qk_norm_rope_write, L.pa_decode_window,
+                                                        L.pa_prefill_varlen_window)])
+        _native_mod = m
+    return _native_mod
 
 
 def _need(t, name, dtype=None, cuda=True):
@@ -269,103 +283,16 @@ class QKTransform:
 
     def __post_init__(self):
         r = self.rope
-        given = []  # (tensor, field of the C struct)
         for name, w in (("q_weight", self.q_weight), ("k_weight", self.k_weight)):
             if w is not None:
                 _need(w, name, torch.float32)
                 if w.dim() != 1:
                     raise ValueError("%s must be [head_size]" % name)
-                given.append((w, name))
         if r is not None:
             _need(r.turns, "rope.turns", torch.int64)
-            given.append((r.turns, "turns"))
-        if len({t.get_device() for t, _ in given}) > 1:
-            raise ValueError("the transform's tensors must be on one device")
-        if len({t.shape[0] for t, f in given if f != "turns"}) > 1:
-            raise ValueError("q_weight and k_weight must have one head size")
-        object.__setattr__(self, "_given", given)
-        object.__setattr__(self, "_c", _QKTransform(eps=float(self.eps), interleaved=1 if self.interleaved else 0,
-                                                    rope_factor=1.0 if r is None else float(r.factor),
-                                                    rotary_dim=0 if r is None else r.rotary_dim))
-
-    def c_struct(self, head_size: int, index: int) -> _QKTransform:
-        c = self._c
-        for t, field in self._given:
-            if t.get_device() != index or (field != "turns" and t.shape[0] != head_size):
-                raise ValueError("the transform's tensors must be on the rows' device, the weights of the rows' head size")
-            setattr(c, field, t.data_ptr())
-        return c
-
-
-_I32, _I64 = torch.int32, torch.int64
-
-
-def _rows(t, name, shape, dtype, index):
-    """Checks [T, heads, head_size] rows whose tokens may be strided; returns
-    the token stride."""
-    if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
-        raise ValueError("%s must be %s %s on device %d" % (name, dtype, tuple(shape), index))
-    st, sh, sd = t.stride()
-    T, n, D = shape
-    if sd != 1 or (sh != D and n > 1):
-        raise ValueError("the heads of a token of %s must be contiguous" % name)
-    return st if T > 1 else max(st, n * D)  # (a single token's stride says nothing)
-
-
-def _rows_of(t, name):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3:
-        raise ValueError("%s must be a CUDA tensor [tokens, heads, head_size]" % name)
-    return t.shape
-
-
-def _vector(t, name, dtype, n, index):
-    """The address of a contiguous [n] tensor of that type on the device."""
-    if t.dtype is not dtype:
-        raise TypeError("%s must be %s" % (name, dtype))
-    if t.shape != (n,) or t.get_device() != index or not t.is_contiguous():
-        raise ValueError("%s must be contiguous [%d] on the queries' device" % (name, n))
-    return t.data_ptr()
-
-
-def _table(t, rows, index):
-    """The address and width of a block table [rows, max_blocks]."""
-    if t.dtype is not _I32:
-        raise TypeError("block_table must be torch.int32")
-    if t.dim() != 2 or t.get_device() != index or not t.is_contiguous():
-        raise ValueError("block_table must be contiguous [num_seqs, max_blocks] on the queries' device")
-    n, width = t.shape
-    if n != rows:
-        raise ValueError("block_table must have %d rows" % rows)
-    return t.data_ptr(), width
-
-
-def _status_ptr(t, index):
-    if t is None:
-        return None
-    if t.dtype is not _I32 or t.get_device() != index:
-        raise ValueError("dev_status must be int32 on the queries' device")
-    return t.data_ptr()
-
-
-def _scratch(t, index):
-    if t is None:
-        return None, 0
-    if t.get_device() != index or not t.is_contiguous():
-        raise ValueError("workspace must be contiguous on the queries' device")
-    return t.data_ptr(), t.numel() * t.element_size()
-
-
-def _queries(q, out, cs, cache):
-    """Checks contiguous q and out [rows, num_heads, head_size] beside the cache
-    (its C struct cs); returns the rows, the heads, the type's code, the device."""
-    shape = _rows_of(q, "q")
-    index, dtype = q.get_device(), q.dtype
-    if out.shape != shape or out.dtype is not dtype or out.get_device() != index or not q.is_contiguous() or \
-            not out.is_contiguous():
-        raise ValueError("q and out must be contiguous and of one shape, type and device")
-    if cs.head_size != shape[2] or cache.k_cache.get_device() != index:
-        raise ValueError("the cache must have the queries' head size and device")
-    return shape[0], shape[1], torch_dtype_code(dtype), index
+        # what the native call reads
+        object.__setattr__(self, "_args", (self.q_weight, self.k_weight, None if r is None else r.turns, float(self.eps),
+                                           1.0 if r is None else float(r.factor), bool(self.interleaved)))
 
 
 def pa_qk_norm_rope(q_out: torch.Tensor, k_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
@@ -374,17 +301,7 @@ def pa_qk_norm_rope(q_out: torch.Tensor, k_out: torch.Tensor, q: torch.Tensor, k
     num_kv_heads, head_size] (tokens may be strided: views of a fused qkv buffer)
     into q_out and k_out of the same shapes, which may be q and k themselves;
     positions: int64 [T]."""
-    shape, kshape = _rows_of(q, "q"), _rows_of(k, "k")
-    T, H, D = shape
-    dt, dev = q.dtype, q.get_device()
-    if kshape[0] != T or kshape[2] != D:
-        raise ValueError("k must have the queries' tokens and head size")
-    qs, ks = _rows(q, "q", shape, dt, dev), _rows(k, "k", kshape, dt, dev)
-    qos, kos = _rows(q_out, "q_out", shape, dt, dev), _rows(k_out, "k_out", kshape, dt, dev)
-    pos = None if positions is None else _vector(positions, "positions", _I64, T, dev)
-    _check(_call(library().pa_qk_norm_rope, dev, q_out.data_ptr(), k_out.data_ptr(), q.data_ptr(), k.data_ptr(),
-                 torch_dtype_code(dt), T, H, kshape[1], D, qs, ks, qos, kos, pos, transform.c_struct(D, dev)),
-           "pa_qk_norm_rope")
+    _check(_native().qk_norm_rope(q_out, k_out, q, k, positions, transform._args), "pa_qk_norm_rope")
 
 
 def pa_qk_norm_rope_write(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: KVCache,
@@ -392,20 +309,8 @@ def pa_qk_norm_rope_write(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
                           dev_status: Optional[torch.Tensor] = None):
     """pa_qk_norm_rope with the keys, and the values v as they are, written to
     slot_mapping's (int64 [T], < 0 skips) slots of the cache."""
-    shape = _rows_of(q, "q")
-    T, H, D = shape
-    dt, dev = q.dtype, q.get_device()
-    cs = cache.c_struct()
-    if D != cs.head_size or cache.k_cache.get_device() != dev:
-        raise ValueError("the cache must have the queries' head size and device")
-    kshape = (T, cs.num_kv_heads, D)
-    qs, ks, vs = _rows(q, "q", shape, dt, dev), _rows(k, "k", kshape, dt, dev), _rows(v, "v", kshape, dt, dev)
-    qos = _rows(q_out, "q_out", shape, dt, dev)
-    pos = None if positions is None else _vector(positions, "positions", _I64, T, dev)
-    _check(_call(library().pa_qk_norm_rope_write, dev, q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                 torch_dtype_code(dt), cs, T, H, qs, ks, vs, qos, pos,
-                 _vector(slot_mapping, "slot_mapping", _I64, T, dev), transform.c_struct(D, dev),
-                 _status_ptr(dev_status, dev)), "pa_qk_norm_rope_write")
+    _check(_native().qk_norm_rope_write(q_out, q, k, v, cache.k_cache, cache.v_cache, cache.k_scale, cache.v_scale,
+                                        positions, slot_mapping, transform._args, dev_status), "pa_qk_norm_rope_write")
 
 
 def pa_copy_blocks(cache: KVCache, src_dst_pairs: torch.Tensor, dev_status: Optional[torch.Tensor] = None):
@@ -522,14 +427,9 @@ def pa_decode_window(out: torch.Tensor, q: torch.Tensor, cache: KVCache, block_t
     """pa_decode where each query sees the last `window` tokens (its own
     included) and the first num_sinks; block-table entries of blocks that hold
     neither are not read."""
-    cs = cache.c_struct()
-    B, H, code, dev = _queries(q, out, cs, cache)
-    table, width = _table(block_table, B, dev)
-    lens = _vector(seq_lens, "seq_lens", _I32, B, dev)
-    ws, ws_bytes = _scratch(workspace, dev)
-    _check(_call(library().pa_decode_window, dev, out.data_ptr(), q.data_ptr(), code, cs, table, width, lens, B,
-                 int(max_seq_len), H, float(scale), int(window), int(num_sinks), int(partition_size), ws, ws_bytes,
-                 _status_ptr(dev_status, dev)), "pa_decode_window")
+    _check(_native().decode_window(out, q, cache.k_cache, cache.v_cache, cache.k_scale, cache.v_scale, block_table,
+                                   seq_lens, max_seq_len, scale, window, num_sinks, partition_size, workspace,
+                                   dev_status), "pa_decode_window")
 
 
 def pa_decode_test_wait_timeout(out: torch.Tensor, q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
@@ -660,15 +560,9 @@ def pa_prefill_varlen_window(out: torch.Tensor, q: torch.Tensor, cache: KVCache,
     """pa_prefill_varlen, causal, where a query at position x sees the keys of
     positions x - window + 1 .. x and the first num_sinks; block-table entries
     of blocks that no query sees are not read."""
-    cs = cache.c_struct()
-    _, H, code, dev = _queries(q, out, cs, cache)
-    B = cu_seq_lens_q.shape[0] - 1
-    cu_q = _vector(cu_seq_lens_q, "cu_seq_lens_q", _I32, B + 1, dev)
-    cu_k = _vector(cu_seq_lens_k, "cu_seq_lens_k", _I32, B + 1, dev)
-    table, width = _table(block_table, B, dev)
-    _check(_call(library().pa_prefill_varlen_window, dev, out.data_ptr(), q.data_ptr(), code, cs, table, width, cu_q, cu_k,
-                 B, int(max_seqlen_q), int(max_seqlen_k), H, float(scale), int(window), int(num_sinks),
-                 _status_ptr(dev_status, dev)), "pa_prefill_varlen_window")
+    _check(_native().prefill_varlen_window(out, q, cache.k_cache, cache.v_cache, cache.k_scale, cache.v_scale,
+                                           block_table, cu_seq_lens_q, cu_seq_lens_k, max_seqlen_q, max_seqlen_k, scale,
+                                           window, num_sinks, dev_status), "pa_prefill_varlen_window")
 
 
 def pa_slot_mapping(block_table, block_size: int, seq_idx, pos):

@@ -8,12 +8,16 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libpa_kv.so")
+# the CPython module that marshals the calls of a decode step
+NATIVE_SRC = os.path.join(PKG, "native", "calls.cpp")
+NATIVE = os.path.join(PKG, "_native.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -38,7 +42,23 @@ def _stale():
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def build_native(force: bool = False) -> str:
+    """The CPython module _native (g++; it links to nothing of the library)."""
+    newest = max(os.path.getmtime(NATIVE_SRC), os.path.getmtime(os.path.join(INCLUDE, "pa_kv.h")))
+    if not force and os.path.exists(NATIVE) and os.path.getmtime(NATIVE) >= newest:
+        return NATIVE
+    tmp = NATIVE + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall", "-I", INCLUDE, "-I",
+           sysconfig.get_paths()["include"], NATIVE_SRC, "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed on %s:\n%s%s" % (NATIVE_SRC, r.stdout, r.stderr))
+    os.replace(tmp, NATIVE)
+    return NATIVE
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_native(force)
     if not force and not _stale():
         return LIB
     nvcc = _nvcc()

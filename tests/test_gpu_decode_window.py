@@ -100,6 +100,29 @@ def test_long_sequences(kind, G, D, bs, P):
     R.check(out, ref, mag)
 
 
+@pytest.mark.parametrize("kind,G,bs", [("f16", 1, 16), ("bf16", 4, 16), ("e4m3", 8, 32), ("bf16", 2, 64)])
+@pytest.mark.parametrize("P", [0, 64, 128])
+def test_more_items_than_blocks(kind, G, bs, P):
+    """A batch whose items the blocks take several of, in the work list's order (smaller ones build no list)."""
+    qd, kd = KINDS[kind]
+    rng = np.random.default_rng(P + G)
+    lens = [int(x) for x in rng.integers(0, 700, size=330)]
+    window, sinks = 260, 9
+    case = W.make_decode_case(4, lens, 2 * G, 2, 64, bs, sum(W.pages_for(x, bs) for x in lens) + 2, qd, kd)
+    kc, vc, table = poison(case, window, sinks)
+    out, st = run(case, window, sinks, P, kc, vc, table)
+    assert st == 0
+    ref, mag = reference(case, window, sinks)
+    R.check(out, ref, mag)
+    # a batch in which one length is beyond the maximum: the others as they were
+    lens[5] = 701
+    broken = W.PagedCase(**{**case.__dict__, "seq_lens": torch.tensor(lens, dtype=torch.int32)})
+    again, st = run(broken, window, sinks, P, kc, vc, table, max_len=700)
+    assert st == 1 and bool((again[5] == 0).all())
+    keep = torch.arange(330) != 5
+    R.check(again[keep], ref[keep], mag[keep])
+
+
 @pytest.mark.parametrize("kind", ["f16", "bf16", "e4m3"])
 @pytest.mark.parametrize("G", [1, 4])
 def test_a_window_of_everything_is_plain_decode(kind, G):
@@ -220,7 +243,79 @@ def test_the_binding_refuses_wrong_tensors():
         pk.pa_decode_window(out, q, cache, table, sl[:1], 30, 0.1, 8)
     with pytest.raises(ValueError):
         pk.pa_decode_window(out, q, cache, table.cpu(), sl, 30, 0.1, 8)
+    with pytest.raises(TypeError):
+        pk.pa_decode_window(out, q, cache, table, sl.long(), 30, 0.1, 8)
+    with pytest.raises(OverflowError):
+        pk.pa_decode_window(out, q, cache, table, sl, 30, 0.1, 1 << 31)
+    with pytest.raises(TypeError):
+        pk.pa_decode_window(out, q, cache, table, sl, 30.5, 0.1, 8)
+    # numpy's numbers are numbers
+    pk.pa_decode_window(out, q, cache, table, sl, np.int64(30), np.float32(0.1), np.int32(8))
     with pytest.raises(pk.PaError):
         pk.pa_decode_window(out, q, cache, table, sl, 30, 0.1, 0)
     with pytest.raises(pk.PaError):
         pk.pa_decode_window(out, q, cache, table, sl, 30, 0.1, 8, -1)
+
+
+def test_calls_on_two_streams_and_threads_at_once():
+    """Two threads, each with a stream, a workspace and inputs of its own."""
+    import threading
+    cases = [W.make_decode_case(20 + i, [900, 77, 400], 8, 2, 128, 16, 100, W.BF16, W.BF16) for i in range(2)]
+    refs = [reference(c, 300, 7) for c in cases]
+    outs, errors = [None, None], []
+
+    def work(i):
+        try:
+            c, s = cases[i], torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                cache, q = pk.KVCache(c.k_cache.to(DEV), c.v_cache.to(DEV)), c.q.to(DEV)
+                table, sl, out = c.block_table.to(DEV), c.seq_lens.to(DEV), torch.empty_like(c.q, device=DEV)
+                n = pk.pa_decode_window_workspace_size(3, 8, 128, 900, 16, 300, 7, 64)
+                ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+                for _ in range(200):
+                    pk.pa_decode_window(out, q, cache, table, sl, 900, c.scale, 300, 7, 64, ws)
+                s.synchronize()
+            outs[i] = out.cpu()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not errors
+    for o, (ref, mag) in zip(outs, refs):
+        R.check(o, ref, mag)
+
+
+def test_blocks_past_four_gigabytes():
+    """Blocks whose byte offset in the cache passes 32 bits: write, decode and prefill."""
+    nb, bs, Hkv, H, D = 1_100_000, 16, 1, 4, 128  # 4.5 GB each of K and V
+    kc = torch.zeros(nb, Hkv, bs, D, dtype=torch.bfloat16, device=DEV)
+    vc = torch.zeros(nb, Hkv, bs, D, dtype=torch.bfloat16, device=DEV)
+    cache = pk.KVCache(kc, vc)
+    g = torch.Generator().manual_seed(0)
+    T = 100
+    ids = [nb - 1, 5, nb - 3, 1_048_577, 1_048_576, nb - 70, 3]
+    x = torch.randn(T, H + 2 * Hkv, D, generator=g).to(torch.bfloat16)
+    slots = torch.tensor([ids[t // bs] * bs + t % bs for t in range(T)])
+    xd = x.to(DEV)
+    q = torch.empty(T, H, D, dtype=torch.bfloat16, device=DEV)
+    st = dev_status()
+    pk.pa_qk_norm_rope_write(q, xd[:, :H], xd[:, H:H + 1], xd[:, H + 1:], cache, None, slots.to(DEV), pk.QKTransform(), st)
+    assert torch.equal(kc[ids[3], 0, 2], xd[50, H]) and torch.equal(vc[nb - 1, 0, 9], xd[9, H + 1])
+    small_k = torch.zeros(7, Hkv, bs, D, dtype=torch.bfloat16)
+    small_v = torch.zeros(7, Hkv, bs, D, dtype=torch.bfloat16)
+    t = torch.arange(T)
+    small_k[t // bs, 0, t % bs], small_v[t // bs, 0, t % bs] = x[:, H], x[:, H + 1]
+    table = torch.tensor([ids], dtype=torch.int32, device=DEV)
+    out = torch.empty_like(q)
+    pk.pa_prefill_varlen_window(out, q, cache, table, torch.tensor([0, T], dtype=torch.int32, device=DEV),
+                                torch.tensor([0, T], dtype=torch.int32, device=DEV), T, T, D ** -0.5, 40, 3, st)
+    ref, mag = R.attend(x[:, :H], range(T), T, torch.arange(7), small_k, small_v, D ** -0.5, 40, 3)
+    R.check(out.cpu(), ref, mag)
+    one = torch.empty(1, H, D, dtype=torch.bfloat16, device=DEV)
+    ws = torch.empty(pk.pa_decode_window_workspace_size(1, H, D, T, bs, 40, 3, 16), dtype=torch.uint8, device=DEV)
+    pk.pa_decode_window(one, q[-1:], cache, table, torch.tensor([T], dtype=torch.int32, device=DEV), T, D ** -0.5, 40, 3, 16,
+                        ws, st)
+    R.check(one.cpu(), ref[-1:], mag[-1:])
+    assert st.item() == 0

@@ -97,6 +97,33 @@ def test_long_chunks(dt, G, bs, window, sinks):
     assert bool(out.isfinite().all())
 
 
+@pytest.mark.parametrize("dt,G,Hkv,bs", [("bf16", 8, 2, 16), ("f16", 4, 4, 32), ("bf16", 1, 8, 64)])
+@pytest.mark.parametrize("window,sinks", [(300, 4), (130, 0), (17, 33)])
+def test_several_items_a_block(dt, G, Hkv, bs, window, sinks):
+    """More items than blocks, of unlike costs: the sorted order, both tensor-memory buffers, the deferred output."""
+    rng = np.random.default_rng(window)
+    lq = [int(x) for x in rng.integers(1, 500, size=14)] + [0, 1, 1, 2000]
+    lk = [n + int(x) for n, x in zip(lq, rng.integers(0, 1500, size=len(lq)))]
+    c = Batch(lq, lk, G, Hkv, bs, TYPES[dt], seed=G)
+    assert sum(-(-n // (128 // G)) for n in lq) * Hkv > 2 * 152
+    rows = {b: sorted({int(i) for i in rng.integers(0, n, size=5)} | {0, n - 1}) for b, n in enumerate(lq) if n}
+    out, st = c.run(window, sinks, *c.poisoned(window, sinks))
+    assert st == 0 and bool(out.isfinite().all())
+    idx, ref, mag = c.reference(window, sinks, rows)
+    R.check(out[idx], ref, mag)
+
+
+def test_more_items_than_a_blocks_table_of_them():
+    """Over 64 items a block: the rest are worked out on the way."""
+    n, lq = 330, 60
+    c = Batch([lq] * n, [lq + 40 + b % 90 for b in range(n)], 8, 8, 16, torch.bfloat16, seed=2)
+    assert n * -(-lq // 16) * 8 > 64 * 152
+    out, st = c.run(50, 3)
+    assert st == 0 and bool(out.isfinite().all())
+    idx, ref, mag = c.reference(50, 3, {b: [0, b % lq, lq - 1] for b in range(0, n, 23)})
+    R.check(out[idx], ref, mag)
+
+
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
 @pytest.mark.parametrize("G", [1, 4])
 def test_a_window_of_everything_is_plain_causal_prefill(dt, G):

@@ -70,6 +70,44 @@ def test_token_counts_and_heads(T, H, Hkv):
         rope_ref.check(got.cpu()[sample], ref, pair, x.dtype)
 
 
+@pytest.mark.parametrize("T", [2431, 2432, 2433, 4864, 7001])
+@pytest.mark.parametrize("D,H,Hkv", [(128, 32, 8), (64, 5, 3), (128, 1, 1)])
+@pytest.mark.parametrize("write", [False, True])
+def test_many_tokens_equal_few(T, D, H, Hkv, write):
+    """Counts around whole rounds of the resident warps (and past several): the same bits as in calls of a few hundred
+    tokens each, which hold no whole round."""
+    dt, bs = torch.bfloat16, 16
+    x, pos, qw, kw = make(T, H, Hkv, D, dt, seed=T)
+    tr = transform(D // 2, D == 64, qw, kw)
+    xd, pd = x.to(DEV), pos.to(DEV)
+    g = torch.Generator().manual_seed(1)
+    nb = T // bs + 2
+    slots = torch.randperm(nb * bs, generator=g)[:T].to(DEV)
+    slots[::11] = -1
+    res = []
+    for step in (T, 300):
+        qo = torch.zeros(T, H, D, dtype=dt, device=DEV)
+        if write:
+            cache = pk.KVCache(torch.zeros(nb, Hkv, bs, D, dtype=dt, device=DEV), torch.zeros(nb, Hkv, bs, D, dtype=dt, device=DEV))
+            out = (qo, cache.k_cache, cache.v_cache)
+        else:
+            ko = torch.zeros(T, Hkv, D, dtype=dt, device=DEV)
+            out = (qo, ko)
+        for a in range(0, T, step):
+            b = min(T, a + step)
+            q, k, v = xd[a:b, :H], xd[a:b, H:H + Hkv], xd[a:b, H + Hkv:]
+            if write:
+                pk.pa_qk_norm_rope_write(qo[a:b], q, k, v, cache, pd[a:b], slots[a:b], tr)
+            else:
+                pk.pa_qk_norm_rope(qo[a:b], ko[a:b], q, k, pd[a:b], tr)
+        res.append(out)
+    for a, b in zip(*res):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+    sample = [0, 1, T // 2, T - 2, T - 1]
+    ref, pair = reference(x[sample, :H], pos[sample], tr, qw)
+    rope_ref.check(res[0][0].cpu()[sample], ref, pair, dt)
+
+
 @pytest.mark.parametrize("kv", ["f16", "bf16", "e4m3"])
 @pytest.mark.parametrize("D,H,Hkv,bs", [(128, 8, 2, 16), (64, 4, 4, 32), (128, 32, 8, 64), (64, 3, 1, 5)])
 @pytest.mark.parametrize("T", [1, 45, 400])
