@@ -602,6 +602,8 @@ pa_status prepare(NormRopeParams& p, void* q_out, const void* q, const void* k, 
     if (num_tokens == 0) return PA_OK;
     if (q_out == nullptr || q == nullptr || k == nullptr || (tr->rotary_dim > 0 && positions == nullptr))
         return PA_ERR_INVALID_ARG;
+    // in place, a token's rows have to stay where they are
+    if (q_out == q && q_out_stride != q_stride && num_tokens > 1) return PA_ERR_INVALID_ARG;
     p.q = static_cast<const uint16_t*>(q);
     p.k = static_cast<const uint16_t*>(k);
     p.q_out = static_cast<uint16_t*>(q_out);
@@ -641,7 +643,7 @@ extern "C" pa_status pa_qk_norm_rope(void* q_out, void* k_out, const void* q, co
     if (st != PA_OK) return st;
     if (k_out_stride < static_cast<int64_t>(num_kv_heads) * head_size) return PA_ERR_INVALID_ARG;
     if (num_tokens == 0) return PA_OK;
-    if (k_out == nullptr) return PA_ERR_INVALID_ARG;
+    if (k_out == nullptr || (k_out == k && k_out_stride != k_stride && num_tokens > 1)) return PA_ERR_INVALID_ARG;
     p.k_out = k_out;
     p.ko_stride = k_out_stride;
     p.ko_vec = aligned16(k_out, k_out_stride);

@@ -77,9 +77,12 @@ def transform(**kw):
     return t
 
 
+OTHER = FAKE + (1 << 12)
+
+
 def _rope(lib, tr, T=3, H=4, Hkv=2, D=128, dt=pk.PA_BF16, qs=512, ks=256, qos=512, kos=256, q=FAKE, pos=FAKE,
-          k_out=FAKE):
-    return lib.pa_qk_norm_rope(FAKE, k_out, q, FAKE, dt, T, H, Hkv, D, qs, ks, qos, kos, pos,
+          k_out=OTHER, q_out=OTHER):
+    return lib.pa_qk_norm_rope(q_out, k_out, q, FAKE, dt, T, H, Hkv, D, qs, ks, qos, kos, pos,
                                None if tr is None else C.byref(tr), None)
 
 
@@ -95,6 +98,8 @@ def test_rope_rejects_bad_arguments_before_launch(lib):
     assert _rope(lib, ok, qs=511) == 1 and _rope(lib, ok, ks=255) == 1
     assert _rope(lib, ok, qos=511) == 1 and _rope(lib, ok, kos=255) == 1
     assert _rope(lib, ok, q=None) == 1 and _rope(lib, ok, pos=None) == 1 and _rope(lib, ok, k_out=None) == 1
+    # in place with another stride
+    assert _rope(lib, ok, q_out=FAKE, qos=520) == 1 and _rope(lib, ok, k_out=FAKE, kos=264) == 1
     assert _rope(lib, transform(rotary_dim=24)) == 2
     assert _rope(lib, transform(rotary_dim=144)) == 1 and _rope(lib, transform(rotary_dim=-16)) == 1
     assert _rope(lib, transform(turns=None)) == 1 and _rope(lib, transform(turns=FAKE + 4)) == 1
