@@ -213,6 +213,23 @@ def test_writes_only_out():
     R.check(go.t.cpu(), ref, mag)
 
 
+@pytest.mark.parametrize("dt,G,bs", [("bf16", 4, 16), ("f16", 8, 32)])
+def test_rows_past_the_last_sequence_stay_as_they_were(dt, G, bs):
+    """A batch padded to a fixed count of rows, as a captured step keeps it: empty sequences at its end, rows behind the
+    last one, in q (NaN) and in out."""
+    c = Batch([37, 1, 70, 0, 0], [137, 20, 300, 0, 0], G, 2, bs, TYPES[dt])
+    pad = 45
+    q = torch.cat([c.q, torch.full((pad, *c.q.shape[1:]), float("nan"), dtype=c.q.dtype)]).to(DEV)
+    out = torch.full_like(q, 7.0)
+    st = dev_status()
+    pk.pa_prefill_varlen_window(out, q, pk.KVCache(c.kc.to(DEV), c.vc.to(DEV)), c.table.to(DEV), c.cu_q.to(DEV),
+                                c.cu_k.to(DEV), 128, 512, c.scale, 60, 3, st)
+    torch.cuda.synchronize()
+    assert st.item() == 0 and bool((out[-pad:] == 7.0).all())
+    idx, ref, mag = c.reference(60, 3)
+    R.check(out[:-pad].cpu()[idx], ref, mag)
+
+
 def test_captured_and_replayed():
     c = Batch([64, 9], [300, 200], 4, 2, 16, torch.bfloat16)
     out = torch.empty_like(c.q).to(DEV)
