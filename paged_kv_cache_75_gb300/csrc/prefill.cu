@@ -1076,6 +1076,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
                 [[maybe_unused]] const int hid1 = WIN ? min(lo - key0, 64) : 0;
                 ok = ok && mbar_wait(s_full + 8 * b, s_use[b] & 1u, p.status, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
+                tc_fence_after();  // for both reads of S below
                 ++s_use[b];
                 float e[64];
                 float sum = 0.f;
@@ -1084,7 +1085,6 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
                 // true maximum)
                 const bool first = WIN && t == 0;
                 if (ok && !first) {
-                    tc_fence_after();
                     tmem_ld64(sbuf + b * kBN, e);
                     hide_keys<WIN>(e, vis, hid0, hid1);
                     if (m == -INFINITY) {

@@ -1,0 +1,49 @@
+"""What orders the prefill kernel's warps, read from its source: faults that no run shows for certain.  No GPU."""
+import os
+import re
+
+import pytest
+
+from paged_kv_cache_75_gb300 import build as pkg_build
+
+
+def without_comments(text):
+    return re.sub(r"//[^\n]*", "", re.sub(r"/\*.*?\*/", "", text, flags=re.S))
+
+
+def before(text, at):
+    """What every path to text[at] passes through: the text before it without the blocks that closed again."""
+    out, depth = [], 0
+    for c in reversed(text[:at]):
+        if c == "}":
+            depth += 1
+        elif c == "{" and depth:
+            depth -= 1
+        elif depth == 0:
+            out.append(c)
+    return "".join(reversed(out))
+
+
+@pytest.fixture(scope="module")
+def kernel():
+    with open(os.path.join(pkg_build.CSRC, "prefill.cu")) as f:
+        text = without_comments(f.read())
+    text = text[text.index("paged_prefill_tc_kernel(const __grid_constant__"):]
+    return text[:text.index("PFN_cuTensorMapEncodeTiled")]
+
+
+def test_the_reading_itself():
+    text = "wait(); if (a) { fence(); } load();"
+    assert "fence" not in before(text, text.index("load")) and "wait" in before(text, text.index("load"))
+    text = "wait(); fence(); if (a) { b(); { load(); } }"
+    assert "fence" in before(text, text.index("load"))
+
+
+def test_tensor_memory_is_read_behind_a_fence(kernel):
+    """A tcgen05.ld or .mma follows another thread's tcgen05 work only behind a tcgen05.fence::after_thread_sync that
+    comes after the wait, on every path."""
+    places = [m.start() for m in re.finditer(r"\b(tmem_ld\d+|mma_f16_\w+)\(", kernel)]
+    assert len(places) >= 6
+    for at in places:
+        path = before(kernel, at)
+        assert path.rfind("tc_fence_after()") > path.rfind("mbar_wait(") >= 0, kernel[at - 200:at + 60]
