@@ -845,8 +845,11 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
         uint32_t pv_count = 0;              // PVs issued so far (all items)
         uint32_t q_cnt = 0;                 // items with tiles
         bool ok = true;
+        // (the warp votes on each wait: one that ran out, or met an abort, in a
+        // single lane ends it for all, since elect.sync and the shuffles behind
+        // the waits want every lane)
         auto issue_qk = [&](int t, bool last) -> bool {
-            if (!mbar_wait(k_full + 8 * k_stage, k_phase, p.status, abort_flag)) return false;
+            if (!__all_sync(0xffffffffu, mbar_wait(k_full + 8 * k_stage, k_phase, p.status, abort_flag))) return false;
             tc_fence_after();
             const uint32_t stage = uniform(k_stage), b = uniform(t & 1);
             if (elect_one()) {
@@ -881,7 +884,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
                 if (item >= 0) w_next = item_work(rnd + 1, item);
                 continue;
             }
-            ok = mbar_wait(q_full, q_cnt & 1u, p.status, abort_flag);
+            ok = __all_sync(0xffffffffu, mbar_wait(q_full, q_cnt & 1u, p.status, abort_flag));
             const uint32_t col_o = tmem + kColO + (q_cnt & 1u) * kD;  // this item's O
             ++q_cnt;
             if (ok) ok = issue_qk(0, w.ntiles == 1);
@@ -890,8 +893,8 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
             if (item >= 0) w_next = item_work(rnd + 1, item);
             for (int t = 0; t < w.ntiles && ok; ++t) {
                 const int y = t & 1;
-                ok = mbar_wait(p_full + 8 * y, p_use[y] & 1u, p.status, abort_flag) &&
-                     mbar_wait(v_full + 8 * v_stage, v_phase, p.status, abort_flag);
+                ok = __all_sync(0xffffffffu, mbar_wait(p_full + 8 * y, p_use[y] & 1u, p.status, abort_flag));
+                ok = ok && __all_sync(0xffffffffu, mbar_wait(v_full + 8 * v_stage, v_phase, p.status, abort_flag));
                 if (!ok) break;
                 ++p_use[y];
                 tc_fence_after();

@@ -47,3 +47,18 @@ def test_tensor_memory_is_read_behind_a_fence(kernel):
     for at in places:
         path = before(kernel, at)
         assert path.rfind("tc_fence_after()") > path.rfind("mbar_wait(") >= 0, kernel[at - 200:at + 60]
+
+
+def test_a_warp_leaves_its_waits_together(kernel):
+    """A wait's outcome can differ from lane to lane (a time limit, an abort flag set meanwhile), and the collectives
+    behind it want every lane: each wait's result is one thread's, broadcast, or a vote of the warp."""
+    waits = [m.start() for m in re.finditer(r"\bmbar_wait\(", kernel)]
+    assert len(waits) >= 8
+    for at in waits:
+        line = kernel[kernel.rfind("\n", 0, at):kernel.index(";", at)]
+        behind = kernel[kernel.index(";", at) + 1:].lstrip()
+        name = re.search(r"(\w+) = [^=]*$", kernel[kernel.rfind("\n", 0, at):at])
+        one = "lane == 0" in line and name and behind.startswith("%s = __shfl_sync(0xffffffffu, %s, 0)" % (2 * name.groups()))
+        vote = "__all_sync(0xffffffffu, mbar_wait(" in line or (
+            name and behind.startswith("%s = __all_sync(0xffffffffu, %s)" % (2 * name.groups())))
+        assert one or vote, line
