@@ -278,10 +278,10 @@ __device__ __forceinline__ uint64_t f2add(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
-// One thread of a converged warp, the same at every call.  The compiler knows
-// the branch on it for a single thread's and keeps what it issues there in uniform
-// registers: with lane == 0 in its place each tcgen05.mma cost 100 to 125 cycles of
-// issue instead of about 64, and the prefill ran 11 to 13 % slower.
+// One thread of a converged warp.  The compiler knows the branch on it for a
+// single thread's and keeps what it issues there in uniform registers: with lane
+// == 0 in its place each tcgen05.mma cost 100 to 125 cycles of issue instead of
+// about 64, and the prefill ran 11 to 13 % slower.
 __device__ __forceinline__ bool elect_one() {
     uint32_t r;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
@@ -828,10 +828,13 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
         // -------------------------------- MMA ---------------------------------
         // per item: S[0] = Q K(0)^T, S[1] = Q K(1)^T, then for each tile t:
         // O[c] (+)= P[t&1] V(t) once both softmax warpgroups have written P over S, followed
-        // by S[t&1] = Q K(t+2)^T.  One thread issues everything, so the tensor
-        // pipe sees each PV before the QK that overwrites its P, and a commit
+        // by S[t&1] = Q K(t+2)^T.  One thread waits and issues everything, so the
+        // tensor pipe sees each PV before the QK that overwrites its P, and a commit
         // after QK(t+2) also covers PV(t).  The commit after an item's last QK
-        // releases the query buffer to the query loader.
+        // releases the query buffer to the query loader.  (A wait's outcome can
+        // differ from lane to lane, and the collectives behind it want every lane:
+        // with all lanes waiting and a vote on each wait, the unwindowed prefill
+        // took 423 us for 389 and the windowed one 229 for 220.)
         const uint32_t id_qk = mma_idesc(DT == PA_BF16 ? 1 : 0, kRows, kBN, 0);
         const uint32_t id_pv = mma_idesc(DT == PA_BF16 ? 1 : 0, kRows, kD, 1);
         // descriptors are built once; a k-step only adds a constant to the
@@ -839,21 +842,18 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
         const uint64_t dk = smem_desc(smem_addr(sK), 16, 1024);
         const uint64_t dv = smem_desc(smem_addr(sV), kBlkBytes, 1024);
         const uint64_t dq = smem_desc(smem_addr(sQ), 16, 1024);
-        uint32_t k_stage = 0, k_phase = 0;  // K ring position of the next QK
-        uint32_t v_stage = 0, v_phase = 0;  // V ring position of the next PV
-        uint32_t p_use[2] = {0, 0};         // P[b] handed over so far
-        uint32_t pv_count = 0;              // PVs issued so far (all items)
-        uint32_t q_cnt = 0;                 // items with tiles
-        bool ok = true;
-        // (the warp votes on each wait: one that ran out, or met an abort, in a
-        // single lane ends it for all, since elect.sync and the shuffles behind
-        // the waits want every lane)
-        auto issue_qk = [&](int t, bool last) -> bool {
-            if (!__all_sync(0xffffffffu, mbar_wait(k_full + 8 * k_stage, k_phase, p.status, abort_flag))) return false;
-            tc_fence_after();
-            const uint32_t stage = uniform(k_stage), b = uniform(t & 1);
-            if (elect_one()) {
-                const uint64_t dks = dk + stage * (kTileBytes >> 4);
+        if (elect_one()) {
+            uint32_t k_stage = 0, k_phase = 0;  // K ring position of the next QK
+            uint32_t v_stage = 0, v_phase = 0;  // V ring position of the next PV
+            uint32_t p_use[2] = {0, 0};         // P[b] handed over so far
+            uint32_t pv_count = 0;              // PVs issued so far (all items)
+            uint32_t q_cnt = 0;                 // items with tiles
+            bool ok = true;
+            auto issue_qk = [&](int t, bool last) -> bool {
+                if (!mbar_wait(k_full + 8 * k_stage, k_phase, p.status, abort_flag)) return false;
+                tc_fence_after();
+                const uint32_t b = t & 1;
+                const uint64_t dks = dk + k_stage * (kTileBytes >> 4);
 #pragma unroll
                 for (int k = 0; k < kD / 16; ++k) {
                     // Q and K: 32 bytes per k-step in a 64-column block
@@ -861,46 +861,44 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
                     mma_f16_ss(tmem + kColS + b * kBN, dq + step, dks + step, id_qk, k > 0 ? 1u : 0u);
                 }
                 mma_commit(s_full + 8 * b);
-                mma_commit(k_empty + 8 * stage);
+                mma_commit(k_empty + 8 * k_stage);
                 if (last) mma_commit(q_empty);
-            }
-            __syncwarp();
-            if (++k_stage == kStages) {
-                k_stage = 0;
-                k_phase ^= 1u;
-            }
-            return true;
-        };
-        // the next item's bookkeeping is done after an item's first QKs, while
-        // the softmax warps work on its first tile, not between two items
-        int item = snake_item(0, n_items);
-        Work w_next{};
-        if (item >= 0) w_next = item_work(0, item);
-        for (int rnd = 0; ok && item >= 0; ++rnd) {
-            const Work w = w_next;
-            const int item2 = snake_item(rnd + 1, n_items);
-            if (w.ntiles == 0) {
+                if (++k_stage == kStages) {
+                    k_stage = 0;
+                    k_phase ^= 1u;
+                }
+                return true;
+            };
+            // the next item's bookkeeping is done after an item's first QKs, while
+            // the softmax warps work on its first tile, not between two items
+            int item = snake_item(0, n_items);
+            Work w_next{};
+            if (item >= 0) w_next = item_work(0, item);
+            for (int rnd = 0; ok && item >= 0; ++rnd) {
+                const Work w = w_next;
+                const int item2 = snake_item(rnd + 1, n_items);
+                if (w.ntiles == 0) {
+                    item = item2;
+                    if (item >= 0) w_next = item_work(rnd + 1, item);
+                    continue;
+                }
+                ok = mbar_wait(q_full, q_cnt & 1u, p.status, abort_flag);
+                const uint32_t col_o = tmem + kColO + (q_cnt & 1u) * kD;  // this item's O
+                ++q_cnt;
+                if (ok) ok = issue_qk(0, w.ntiles == 1);
+                if (ok && w.ntiles > 1) ok = issue_qk(1, w.ntiles == 2);
                 item = item2;
                 if (item >= 0) w_next = item_work(rnd + 1, item);
-                continue;
-            }
-            ok = __all_sync(0xffffffffu, mbar_wait(q_full, q_cnt & 1u, p.status, abort_flag));
-            const uint32_t col_o = tmem + kColO + (q_cnt & 1u) * kD;  // this item's O
-            ++q_cnt;
-            if (ok) ok = issue_qk(0, w.ntiles == 1);
-            if (ok && w.ntiles > 1) ok = issue_qk(1, w.ntiles == 2);
-            item = item2;
-            if (item >= 0) w_next = item_work(rnd + 1, item);
-            for (int t = 0; t < w.ntiles && ok; ++t) {
-                const int y = t & 1;
-                ok = __all_sync(0xffffffffu, mbar_wait(p_full + 8 * y, p_use[y] & 1u, p.status, abort_flag));
-                ok = ok && __all_sync(0xffffffffu, mbar_wait(v_full + 8 * v_stage, v_phase, p.status, abort_flag));
-                if (!ok) break;
-                ++p_use[y];
-                tc_fence_after();
-                const uint32_t stage = uniform(v_stage), b = uniform(y), o = uniform(col_o);
-                if (elect_one()) {
-                    const uint64_t dvs = dv + stage * (kTileBytes >> 4);
+                for (int t = 0; t < w.ntiles && ok; ++t) {
+                    const int y = t & 1;
+                    // (V has mostly landed by the time the weights are there: the other way
+                    // round the windowed prefill ran 2 % slower)
+                    ok = mbar_wait(v_full + 8 * v_stage, v_phase, p.status, abort_flag) &&
+                         mbar_wait(p_full + 8 * y, p_use[y] & 1u, p.status, abort_flag);
+                    if (!ok) break;
+                    ++p_use[y];
+                    tc_fence_after();
+                    const uint64_t dvs = dv + v_stage * (kTileBytes >> 4);
                     constexpr int kParts = DT == PA_BF16 ? 2 : 1;  // bf16: hi and lo weights
 #pragma unroll
                     for (int part = 0; part < kParts; ++part) {
@@ -908,24 +906,23 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
                         for (int j = 0; j < kBN / 16; ++j) {
                             // keys 16j..16j+15: P at 8 columns of half j/4 (hi at +0, lo at +32);
                             // V: 2048 bytes per 16 keys
-                            mma_f16_ts(o, tmem + kColS + b * kBN + (j / 4) * 64 + part * 32 + (j % 4) * 8,
+                            mma_f16_ts(col_o, tmem + kColS + y * kBN + (j / 4) * 64 + part * 32 + (j % 4) * 8,
                                        dvs + j * (2048 >> 4), id_pv, (t > 0 || part > 0 || j > 0) ? 1u : 0u);
                         }
                     }
-                    mma_commit(v_empty + 8 * stage);
+                    mma_commit(v_empty + 8 * v_stage);
                     mma_commit(o_done + 8 * (pv_count & 1u));
+                    ++pv_count;
+                    if (++v_stage == kStagesV) {
+                        v_stage = 0;
+                        v_phase ^= 1u;
+                    }
+                    if (t + 2 < w.ntiles) ok = issue_qk(t + 2, t + 3 == w.ntiles);
                 }
-                __syncwarp();
-                ++pv_count;
-                if (++v_stage == kStagesV) {
-                    v_stage = 0;
-                    v_phase ^= 1u;
-                }
-                if (t + 2 < w.ntiles) ok = issue_qk(t + 2, t + 3 == w.ntiles);
             }
+            // every MMA issued here is complete before tensor memory is freed
+            mma_commit(mma_done);
         }
-        // every MMA this warp issued is complete before tensor memory is freed
-        if (elect_one()) mma_commit(mma_done);
         __syncwarp();
         const uint64_t t0 = global_timer_ns();
         while (!mbar_try_wait(mma_done, 0u))

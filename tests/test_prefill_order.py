@@ -51,14 +51,24 @@ def test_tensor_memory_is_read_behind_a_fence(kernel):
 
 def test_a_warp_leaves_its_waits_together(kernel):
     """A wait's outcome can differ from lane to lane (a time limit, an abort flag set meanwhile), and the collectives
-    behind it want every lane: each wait's result is one thread's, broadcast, or a vote of the warp."""
+    behind it want every lane: each wait's result stays with one elected thread, is broadcast from one lane, or is a
+    vote of the warp."""
     waits = [m.start() for m in re.finditer(r"\bmbar_wait\(", kernel)]
     assert len(waits) >= 8
     for at in waits:
+        if "if (elect_one()) {" in before(kernel, at):
+            continue
         line = kernel[kernel.rfind("\n", 0, at):kernel.index(";", at)]
         behind = kernel[kernel.index(";", at) + 1:].lstrip()
         name = re.search(r"(\w+) = [^=]*$", kernel[kernel.rfind("\n", 0, at):at])
         one = "lane == 0" in line and name and behind.startswith("%s = __shfl_sync(0xffffffffu, %s, 0)" % (2 * name.groups()))
-        vote = "__all_sync(0xffffffffu, mbar_wait(" in line or (
-            name and behind.startswith("%s = __all_sync(0xffffffffu, %s)" % (2 * name.groups())))
+        vote = name and behind.startswith("%s = __all_sync(0xffffffffu, %s)" % (2 * name.groups()))
         assert one or vote, line
+
+
+def test_an_elected_thread_meets_no_collective(kernel):
+    """What one thread runs holds nothing that waits for the rest of its warp."""
+    places = [m.start() for m in re.finditer(r"(\w+_sync|__syncwarp|elect_one|bar_red_or|named_bar_\w+|uniform)\(", kernel)]
+    assert len(places) >= 10
+    for at in places:
+        assert "if (elect_one()) {" not in before(kernel, at), kernel[at - 100:at + 60]
