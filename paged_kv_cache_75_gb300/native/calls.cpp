@@ -235,28 +235,33 @@ bool transform_of(PyObject* o, int64_t* index, int64_t head_size, pa_qk_transfor
 // call(stream) on the device `index` and its current stream -> the status
 template <typename Call>
 PyObject* on_device(int64_t index, Call call) {
-    PyObject* cur = PyObject_CallNoArgs(f_get_device);
-    if (cur == nullptr) return nullptr;
     PyObject* want = PyLong_FromLongLong(index);
-    const bool other = PyLong_AsLongLong(cur) != index;
-    PyObject* done = other ? PyObject_CallOneArg(f_set_device, want) : Py_NewRef(Py_None);
-    PyObject* s = done != nullptr ? PyObject_CallOneArg(f_stream, want) : nullptr;
-    pa_status st = PA_ERR_CUDA;
+    PyObject* cur = want != nullptr ? PyObject_CallNoArgs(f_get_device) : nullptr;
+    PyObject* s = cur != nullptr ? PyObject_CallOneArg(f_stream, want) : nullptr;
+    PyObject* result = nullptr;
     if (s != nullptr) {
-        const pa_stream_t stream = static_cast<pa_stream_t>(PyLong_AsVoidPtr(s));
-        Py_BEGIN_ALLOW_THREADS;
-        st = call(stream);
-        Py_END_ALLOW_THREADS;
-    }
-    if (other && done != nullptr) {
-        PyObject* back = PyObject_CallOneArg(f_set_device, cur);
-        Py_XDECREF(back);
+        const int64_t now = PyLong_AsLongLong(cur);
+        const pa_stream_t stream = PyErr_Occurred() ? nullptr : static_cast<pa_stream_t>(PyLong_AsVoidPtr(s));
+        if (!PyErr_Occurred()) {
+            // (from here to the device's restoring nothing but these two can fail:
+            // no Python code runs with an error pending)
+            PyObject* set = now != index ? PyObject_CallOneArg(f_set_device, want) : Py_NewRef(Py_None);
+            if (set != nullptr) {
+                pa_status st;
+                Py_BEGIN_ALLOW_THREADS;
+                st = call(stream);
+                Py_END_ALLOW_THREADS;
+                PyObject* back = now != index ? PyObject_CallOneArg(f_set_device, cur) : Py_NewRef(Py_None);
+                if (back != nullptr) result = PyLong_FromLong(st);
+                Py_XDECREF(back);
+            }
+            Py_XDECREF(set);
+        }
     }
     Py_XDECREF(s);
-    Py_XDECREF(done);
-    Py_DECREF(want);
-    Py_DECREF(cur);
-    return PyErr_Occurred() ? nullptr : PyLong_FromLong(st);
+    Py_XDECREF(cur);
+    Py_XDECREF(want);
+    return result;
 }
 
 bool count(Py_ssize_t got, Py_ssize_t want) {
