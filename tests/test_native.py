@@ -70,9 +70,10 @@ def with_runtime(tmp_path, get_device, set_device, get_stream):
     import ctypes
     import importlib.util
     import shutil
+    import tempfile
 
     pkg_build.build()
-    path = shutil.copy(pkg_build.NATIVE, str(tmp_path))
+    path = shutil.copy(pkg_build.NATIVE, tempfile.mkdtemp(dir=tmp_path))  # (a loaded file is not written over)
     spec = importlib.util.spec_from_file_location("_native", path)
     m = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(m)
