@@ -141,7 +141,7 @@ def _native():
         try:
             from . import _native as m
         except ImportError as e:
-            raise RuntimeError("_native.so is missing: run __graft_entry__.build() "
+            raise RuntimeError("_native is missing: run __graft_entry__.build() "
                                "(or python -m paged_kv_cache_75_gb300.build)") from e
         L = library()
         m.setup(torch.float16, torch.bfloat16, torch.float8_e4m3fn, torch.int32, torch.int64, torch.float32,

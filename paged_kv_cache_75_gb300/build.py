@@ -4,6 +4,7 @@ Each translation unit compiles in parallel; the shared library links the
 CUDA runtime statically so that it only needs the driver at run time.
 """
 import concurrent.futures as cf
+import contextlib
 import glob
 import os
 import shutil
@@ -17,7 +18,9 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libpa_kv.so")
 # the CPython module that marshals the calls of a decode step
 NATIVE_SRC = os.path.join(PKG, "native", "calls.cpp")
-NATIVE = os.path.join(PKG, "_native.so")
+# (named for the interpreter that it is built for: another one does not find it
+# and builds its own)
+NATIVE = os.path.join(PKG, "_native" + sysconfig.get_config_var("EXT_SUFFIX"))
 BUILD_DIR = os.path.join(ROOT, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -54,6 +57,9 @@ def build_native(force: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError("g++ failed on %s:\n%s%s" % (NATIVE_SRC, r.stdout, r.stderr))
     os.replace(tmp, NATIVE)
+    # the name of earlier builds, which any interpreter would load
+    with contextlib.suppress(FileNotFoundError):
+        os.remove(os.path.join(PKG, "_native.so"))
     return NATIVE
 
 

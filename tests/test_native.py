@@ -120,3 +120,13 @@ def test_a_runtime_that_answers_no_number(tmp_path):
     with pytest.raises(TypeError):
         call()
     assert at == [] or at[-1] == 0
+
+
+def test_the_module_is_named_for_its_interpreter(native):
+    """Another Python in the same tree must not load a module built for this one."""
+    import importlib.machinery
+    import os
+
+    assert os.path.samefile(native.__file__, pkg_build.NATIVE)
+    assert os.path.basename(pkg_build.NATIVE) == "_native" + importlib.machinery.EXTENSION_SUFFIXES[0]
+    assert not os.path.exists(os.path.join(pkg_build.PKG, "_native.so"))
