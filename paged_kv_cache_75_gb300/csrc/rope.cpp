@@ -19,11 +19,14 @@ constexpr double kTwoPi = 6.283185307179586476925286766559;
 
 bool positive(double x) { return std::isfinite(x) && x > 0.0; }
 
-// turns per position as a fraction of 2^64 (whole turns leave no trace)
+// turns per position as a fraction of 2^64 (whole turns leave no trace).  Of a
+// negative theta, the complement of -theta's: t - floor(t) would round a small
+// one to 53 bits next to 1, off by 2^-54 of a turn at every position.
 uint64_t fixed_turns(double theta) {
-    const double t = theta / kTwoPi;
+    const double t = std::fabs(theta) / kTwoPi;
     const double frac = std::floor(std::ldexp(t - std::floor(t), 64) + 0.5);
-    return frac >= 18446744073709551616.0 ? 0ull : static_cast<uint64_t>(frac);
+    const uint64_t turns = frac >= 18446744073709551616.0 ? 0ull : static_cast<uint64_t>(frac);
+    return theta < 0.0 ? 0ull - turns : turns;
 }
 
 }  // namespace

@@ -142,3 +142,13 @@ def test_reference_rotation_keeps_lengths_and_relative_angles():
         assert abs((a * b).sum() - (c * d).sum()) < 1e-10
     n, _ = rope_ref.rows(x, [0], th, weight=torch.ones(64), eps=0.0)
     assert abs(n.pow(2).mean() - 1.0) < 1e-12
+
+
+def test_turns_of_a_negative_frequency_are_as_fine(lib):
+    """theta and -theta turn by the same angle the two ways at any position: a small negative frequency keeps the bits
+    that a small positive one has."""
+    th = [1.0, 1e-3, 1e-6, 1e-9, 1e-12, 3.7e-15, 0.25, 6.5]
+    up = pk.rope_frequencies(16, scaling="given", device="cpu", theta=th).turns.numpy().view(np.uint64)
+    down = pk.rope_frequencies(16, scaling="given", device="cpu", theta=[-x for x in th]).turns.numpy().view(np.uint64)
+    for u, d in zip(up, down):
+        assert (int(u) + int(d)) % 2 ** 64 == 0
