@@ -390,23 +390,25 @@ __device__ __forceinline__ void do_steps(const NormRopeParams& p, Run<KVT, D>& u
                 float ss = s2.x + s2.y;
 #pragma unroll
                 for (int d = 1; d < LPR; d <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-                float r = rsqrtf(fmaf(ss, 1.f / D, p.eps));
-                // squares past fp32's range (bf16 rows beyond 10^18): again on
-                // the row scaled by 2^-70, next to which eps is nothing
-                const bool big = !(ss < INFINITY);
-                if (__any_sync(0xffffffffu, big)) {
-                    const float down = big ? 8.470329472543003e-22f : 1.f;
-                    const uint64_t d2 = pair2(down, down);
+                const float ms = fmaf(ss, 1.f / D, p.eps);
+                float r = rsqrtf(ms);
+                // squares, or a sum of squares and eps, past fp32's range on either
+                // side (bf16 rows beyond 10^18; rows below 10^-15 with an eps as
+                // small): again on the row scaled by a power of two, eps by its square
+                const bool far = !(ms > 1.262177448e-29f && ms < INFINITY);  // 2^-96
+                if (__any_sync(0xffffffffu, far)) {
+                    const float by = !far ? 1.f : ms < 1.f ? 1.180591621e+21f : 8.470329473e-22f;  // 2^70, 2^-70
+                    const uint64_t by2 = pair2(by, by);
                     float sd = 0.f;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        y[e] = mul2(y[e], d2);
+                        y[e] = mul2(y[e], by2);
                         const float2 f = unpair2(y[e]);
                         sd = fmaf(f.x, f.x, fmaf(f.y, f.y, sd));
                     }
 #pragma unroll
                     for (int d = 1; d < LPR; d <<= 1) sd += __shfl_xor_sync(0xffffffffu, sd, d);
-                    if (big) r = rsqrtf(sd * (1.f / D));
+                    if (far) r = rsqrtf(fmaf(sd, 1.f / D, p.eps * by * by));
                 }
                 r2 = pair2(r, r);
             }

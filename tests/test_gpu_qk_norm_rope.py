@@ -391,3 +391,21 @@ def test_the_binding_refuses_wrong_tensors():
                        torch.zeros(2, Hkv, 16, 64, dtype=torch.float16, device=DEV))
     with pytest.raises(ValueError):
         pk.pa_qk_norm_rope_write(qo, q, k, k, cache, pd, torch.arange(T, device=DEV), tr)
+
+
+@pytest.mark.parametrize("size,eps", [(2e19, 1e38), (3e18, 3.3e38), (3e38, 3.4e38), (1.0, 3e38), (1e-3, 1e-30), (1e-18, 1e-36),
+                                      (1e-21, 1e-45), (2e-22, 1e-45), (1e-25, 1e-45), (1e-37, 1e-40), (3e-39, 1e-20), (3e-39, 1e-45)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_eps_and_rows_of_any_size(size, eps, interleaved):
+    """Any eps > 0 beside any row: neither the sum of the two nor the squares need fit binary32."""
+    T, H, Hkv, D = 5, 3, 2, 64
+    x, pos, qw, kw = make(T, H, Hkv, D, torch.bfloat16, seed=4)
+    x = (x.float() / x.float().abs().max() * size).to(torch.bfloat16)
+    x[1, 0], x[2] = 0.0, torch.randn(H + 2 * Hkv, D, generator=torch.Generator().manual_seed(1))
+    tr = transform(32, interleaved, qw, kw, eps=float(np.float32(eps)))
+    xd = x.to(DEV)
+    qo, ko = torch.empty(T, H, D, dtype=x.dtype, device=DEV), torch.empty(T, Hkv, D, dtype=x.dtype, device=DEV)
+    pk.pa_qk_norm_rope(qo, ko, xd[:, :H], xd[:, H:H + Hkv], pos.to(DEV), tr)
+    for got, src, w in ((qo, x[:, :H], qw), (ko, x[:, H:H + Hkv], kw)):
+        ref, pair = reference(src, pos, tr, w)
+        rope_ref.check(got.cpu(), ref, pair, x.dtype)
