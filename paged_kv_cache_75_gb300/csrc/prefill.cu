@@ -940,8 +940,8 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
         // only then (and on an item's first tile, where m is -inf) do both
         // warpgroups take the tile's true row max, swap it through shared
         // memory, move m, rescale O and recompute.  Between such events the
-        // weights may grow up to 2^58 against m, well inside fp32 and bf16
-        // range, so no precision is lost.  Every thread of both warpgroups
+        // weights may grow up to 2^64 against m (2^15 where they are fp16), inside
+        // the range of their type, so no precision is lost.  Every thread of both warpgroups
         // passes the same barriers whatever its waits returned, and stops only
         // on an abort snapshot taken right after the previous barrier.
         // An item's epilogue (O / l out of its O buffer) is deferred to the top
@@ -958,7 +958,9 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
         uint32_t n_tiled = 0;  // items with key tiles so far (O[n_tiled & 1] is the current item's)
         uint32_t nbar = 0;     // barriers passed (same count in all 256 threads)
         uint32_t tiles = 0;    // key tiles (= PVs) before the current item
-        constexpr float kSafe = 18446744073709551616.f;  // 2^64: partial sums below it need no new max
+        // partial sums below it need no new max: 2^64, or 2^15 of fp16 weights,
+        // which end at 65504 (a sum is at least its largest weight)
+        constexpr float kSafe = DT == PA_BF16 ? 18446744073709551616.f : 32768.f;
         // after every barrier among the 256: the abort snapshot of the previous one
         auto snapshot = [&]() -> bool {
             const int stop = snap[(nbar + 1) & 1];
