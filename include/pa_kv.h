@@ -366,9 +366,9 @@ pa_status pa_prefill_varlen(void* out, const void* q, pa_dtype q_dtype, const pa
  *     j <= x   with   j > x - window   or   j < num_sinks.
  * A window of max_seqlen_k or more gives pa_prefill_varlen's causal result.
  * Block-table entries of blocks that no query of the sequence sees are not read,
- * and positions that none of them sees may hold anything (NaN included).  A value
- * that some query sees has to be finite for the other queries of the sequence too
- * (a weight of zero still multiplies it).
+ * and what a query does not see takes no part in its output, whatever it is (infinite
+ * or NaN, and also where other queries see it).  A value that is not finite and that
+ * a query sees costs time: the rows that share its tiles are worked out one by one.
  * scale > 0.  Everything else as pa_prefill_varlen (head_size 128).
  * ------------------------------------------------------------------------- */
 pa_status pa_prefill_varlen_window(void* out, const void* q, pa_dtype q_dtype, const pa_kv_cache* cache,

@@ -125,6 +125,8 @@ struct PrefillParams {
 // compiler spill 20 bytes more in their softmax.)
 struct WindowParams : PrefillParams {
     int32_t window, sinks, head;
+    const uint16_t* k_cache;  // (redo_rows)
+    const uint16_t* v_cache;
 };
 template <bool WIN>
 using ParamsOf = std::conditional_t<WIN, WindowParams, PrefillParams>;
@@ -537,6 +539,132 @@ __device__ __forceinline__ void hide_keys(float (&e)[64], int vis, int hid0, int
     }
 }
 
+// Sliding window: rows whose O came out infinite or NaN although the sum of their
+// weights is finite, from the definition.  In a tile's product a weight of zero
+// still multiplies the value of a key that only other rows of the item see, so a
+// value there that is not finite reaches them all; and values near the type's end
+// can overflow under weights that are not divided by their sum yet.  Such rows are
+// found in `out`, and a warp takes one at a time, four columns a lane.  First the
+// values that the row does see: where one is not finite it is the output, no weight
+// being zero.  For what that leaves, the scores of 32 keys, one a lane, once for their
+// maximum and sum and again for the values under divided weights.  qs: 128 floats of
+// this warp in shared memory.  (8192 tokens, 32/8 heads, window 2048: one infinite
+// value in one KV head 10 ms in place of 0.28, one in every block 22 ms.)
+template <int DT>
+__device__ __forceinline__ void redo_rows(const WindowParams& p, const int32_t* prefix, const int32_t* order,
+                                          int n_items, float* qs) {
+    const int lane = threadIdx.x & 31;
+    for (int rnd = 0, item; (item = snake_item(rnd, n_items)) >= 0; ++rnd) {
+        const Work w = work_item<true>(p, prefix, order, item);
+        const int32_t* table = p.block_table + static_cast<int64_t>(w.b) * p.max_blocks;
+        for (int r = threadIdx.x >> 5; r < kRows; r += kThreads / 32) {
+            const int qi = w.i0 + r / p.group, head = w.kvh * p.group + r % p.group;
+            if (qi >= w.lq) break;
+            const int64_t at = (static_cast<int64_t>(w.q0 + qi) * p.num_heads + head) * kD + 4 * lane;
+            uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at);
+            const float2 o01 = kv_pair<DT>(dst->x), o23 = kv_pair<DT>(dst->y);
+            const bool good = fabsf(o01.x) < INFINITY && fabsf(o01.y) < INFINITY && fabsf(o23.x) < INFINITY &&
+                              fabsf(o23.y) < INFINITY;
+            if (__all_sync(0xffffffffu, good)) continue;
+            // the row's n keys: the sinks before its window, then the window
+            const int pos = w.lk - w.lq + qi, lo = first_key<true>(p, pos), first = min(p.sinks, lo);
+            const int n = first + pos + 1 - lo;
+            // key number v's row in the cache, -1: in a block that the loaders reported
+            auto row_of = [&](int v) -> int64_t {
+                const int j = v < first ? v : v - first + lo;
+                const int id = __ldg(table + j / p.block_size);
+                if (id < 0 || id >= p.num_blocks) return -1;
+                return ((static_cast<int64_t>(id) * p.num_kv_heads + w.kvh) * p.block_size + j % p.block_size) * kD;
+            };
+            // its values of this lane's columns (0 for none; no branch, so that loads run ahead)
+            auto value = [&](int64_t row, float (&x)[4]) {
+                const uint2 raw = *reinterpret_cast<const uint2*>(p.v_cache + max(row, int64_t{0}) + 4 * lane);
+                const float2 a = kv_pair<DT>(raw.x), b = kv_pair<DT>(raw.y);
+                x[0] = row < 0 ? 0.f : a.x;
+                x[1] = row < 0 ? 0.f : a.y;
+                x[2] = row < 0 ? 0.f : b.x;
+                x[3] = row < 0 ? 0.f : b.y;
+            };
+            // sums of the values that are not finite: one such value, or NaN
+            float odd[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int v = 0; v < n; v += 32) {
+                const int64_t mine = v + lane < n ? row_of(v + lane) : -1;
+#pragma unroll 8
+                for (int i = 0; i < 32; ++i) {
+                    float x[4];
+                    value(__shfl_sync(0xffffffffu, mine, i), x);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) odd[c] += fabsf(x[c]) < INFINITY ? 0.f : x[c];
+                }
+            }
+            const float was[4] = {o01.x, o01.y, o23.x, o23.y};
+            float acc[4];
+            bool left = false;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                acc[c] = odd[c] == 0.f ? was[c] : odd[c];
+                left |= odd[c] == 0.f && !(fabsf(was[c]) < INFINITY);
+            }
+            if (!__any_sync(0xffffffffu, left)) {
+                *dst = make_uint2(pack2<DT>(acc[0], acc[1]), pack2<DT>(acc[2], acc[3]));
+                continue;
+            }
+            const uint2 qw = *reinterpret_cast<const uint2*>(p.q + at);
+            const float2 q01 = kv_pair<DT>(qw.x), q23 = kv_pair<DT>(qw.y);
+            __syncwarp();
+            *reinterpret_cast<float4*>(qs + 4 * lane) = make_float4(q01.x, q01.y, q23.x, q23.y);
+            __syncwarp();
+            auto score = [&](int v, int64_t& row) -> float {
+                row = v < n ? row_of(v) : -1;
+                if (row < 0) return -INFINITY;
+                const uint4* k = reinterpret_cast<const uint4*>(p.k_cache + row);
+                float sc = 0.f;
+#pragma unroll 4
+                for (int c = 0; c < kD / 8; ++c) {
+                    const uint4 x = k[c];
+                    const float4 a = *reinterpret_cast<const float4*>(qs + 8 * c);
+                    const float4 b = *reinterpret_cast<const float4*>(qs + 8 * c + 4);
+                    const float2 k0 = kv_pair<DT>(x.x), k1 = kv_pair<DT>(x.y), k2 = kv_pair<DT>(x.z), k3 = kv_pair<DT>(x.w);
+                    sc = fmaf(a.x, k0.x, fmaf(a.y, k0.y, fmaf(a.z, k1.x, fmaf(a.w, k1.y, sc))));
+                    sc = fmaf(b.x, k2.x, fmaf(b.y, k2.y, fmaf(b.z, k3.x, fmaf(b.w, k3.y, sc))));
+                }
+                return sc * p.scale_log2;
+            };
+            auto weight = [](float sc, float m) { return sc == -INFINITY ? 0.f : ex2(sc - m); };
+            int64_t row;
+            float m = -INFINITY, l = 0.f;
+            for (int v = lane; v < n; v += 32) {
+                const float sc = score(v, row), top = fmaxf(m, sc);
+                l = l * weight(m, top) + weight(sc, top);
+                m = top;
+            }
+            float top = m;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            l *= weight(m, top);
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[c] = 0.f;
+            for (int v = 0; v < n; v += 32) {
+                const float mine = weight(score(v + lane, row), top) * inv;
+#pragma unroll 8
+                for (int i = 0; i < 32; ++i) {
+                    const float wt = __shfl_sync(0xffffffffu, mine, i);
+                    float x[4];
+                    value(__shfl_sync(0xffffffffu, row, i), x);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) acc[c] = fmaf(wt, x[c], acc[c]);
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[c] = odd[c] == 0.f ? acc[c] : odd[c];
+            *dst = make_uint2(pack2<DT>(acc[0], acc[1]), pack2<DT>(acc[2], acc[3]));
+        }
+    }
+}
+
 // PACKED: K and V are contiguous [Σk][num_kv_heads][head_size] tensors indexed
 // by cu_seq_lens_k (no cache, no block table); otherwise the paged cache.
 // WIN: causal with a sliding window and sinks (an instantiation of its own, so
@@ -566,6 +694,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
     volatile int* snap = reinterpret_cast<volatile int*>(smem + kOffMisc + 8);  // [2] abort snapshots
+    [[maybe_unused]] volatile int* redo = reinterpret_cast<volatile int*>(smem + kOffMisc + 16);  // redo_rows has work
     float* xch = reinterpret_cast<float*>(smem + kOffXch);
     int64_t* pend_off = reinterpret_cast<int64_t*>(smem + kOffPend);        // pending epilogue: out offset (-1: no row)
     float* pend_l = reinterpret_cast<float*>(smem + kOffPend + 256 * 8);     // and partial row sum, per thread
@@ -595,6 +724,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
         mbar_init(q_empty, 1);
         mbar_init(mma_done, 1);
         *abort_flag = 0;
+        *redo = 0;
         snap[0] = 0;
         snap[1] = 0;
         fence_mbar_init();
@@ -1005,10 +1135,15 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
                 // 32-byte stores (whole sectors) when out allows them: a row's
                 // 16 columns start at a multiple of 32 bytes from out
                 const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
+                [[maybe_unused]] uint64_t zero = 0ull;  // NaN once an element is not finite
 #pragma unroll
                 for (int c0 = 0; c0 < 64; c0 += 32) {
                     float o[32];
                     tmem_ld32(o_col + c0, o);
+                    if constexpr (WIN) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) zero = f2fma(f2pack(o[j], o[j + 1]), 0ull, zero);
+                    }
                     if (my_off >= 0) {
                         uint32_t wv[16];
 #pragma unroll
@@ -1023,6 +1158,10 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
                                     make_uint4(wv[4 * j], wv[4 * j + 1], wv[4 * j + 2], wv[4 * j + 3]);
                         }
                     }
+                }
+                if constexpr (WIN) {
+                    const float2 z = f2unpack(zero);
+                    if (my_off >= 0 && !(z.x + z.y == 0.f) && L < INFINITY) *redo = 1;
                 }
                 // a later item's first PV overwrites this O buffer: its p_full
                 // arrival orders that after these reads
@@ -1258,6 +1397,10 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
     __syncthreads();
     tc_fence_after();
     if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+    if constexpr (WIN) {
+        // (every copy has landed and been used: the K ring's memory is free)
+        if (*redo && !*abort_flag) redo_rows<DT>(p, prefix, order, n_items, reinterpret_cast<float*>(sK) + warp * kD);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -1432,7 +1575,8 @@ pa_status prefill_entry(void* out, const void* q, pa_dtype q_dtype, const pa_kv_
     if (window > 0) {
         // (a window, or sinks, past the longest sequence change nothing more)
         const int32_t most = max_seqlen_k > 1 ? max_seqlen_k : 1;
-        WindowParams w{p, window < most ? window : most, sinks < most ? sinks : most, 0};
+        WindowParams w{p, window < most ? window : most, sinks < most ? sinks : most, 0,
+                       static_cast<const uint16_t*>(cache->k_cache), static_cast<const uint16_t*>(cache->v_cache)};
         w.head = (w.sinks + bs - 1) / bs;
         return launch_prefill<false, true>(w, q_dtype, map_k, map_v, map_q, stream);
     }
