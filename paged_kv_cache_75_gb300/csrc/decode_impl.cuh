@@ -747,7 +747,7 @@ __device__ __forceinline__ void decode_consumer_mma(const DecodeParams& p, uint8
         bool ok = __all_sync(0xffffffffu, mbar_wait(qfull0 + 8u * slot, (qn >> 1) & 1u, p.status, abort_flag));
         // ---- Q^T fragments: head gi, span [W*ti, W*ti + W) as pairs ----
         uint32_t qb[KS][2];
-        float qk_scale = p.qk_scale;
+        float qk_scale0 = p.qk_scale, qk_scale1 = p.qk_scale;  // of heads 2ti and 2ti+1
         {
             const int qh = PACK ? (gi & 3) : gi;  // the head of MMA column gi
             const uint8_t* qs = qbuf + slot * QSLOT + (qh * D + W * ti) * C::QB;
@@ -762,9 +762,10 @@ __device__ __forceinline__ void decode_consumer_mma(const DecodeParams& p, uint8
                     qb[2 * c + 1][1] = x.w;
                 }
             } else {
-                // E4M3 cache: queries to fp16 scaled by a power of two so that
-                // the largest lands in [2^14, 2^15); the scale is folded back
-                // into the score scale
+                // E4M3 cache: queries to fp16, a head's scaled by a power of two so
+                // that its largest lands in [2^14, 2^15) (exact but for components
+                // 2^28 times smaller than that one); the scale is folded back into
+                // the head's score scale
                 float qv[W];
                 float mx = 0.f;
 #pragma unroll
@@ -776,11 +777,12 @@ __device__ __forceinline__ void decode_consumer_mma(const DecodeParams& p, uint8
                     mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
                 }
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                for (int o = 1; o < 4; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
                 int ex = mx > 0.f ? ((__float_as_int(mx) >> 23) & 0xff) - 127 - 14 : 0;
                 ex = max(-100, min(100, ex));
                 const float down = __int_as_float((127 - ex) << 23), up = __int_as_float((127 + ex) << 23);
-                qk_scale *= up;
+                qk_scale0 *= __shfl_sync(0xffffffffu, up, 8 * ti);
+                qk_scale1 *= __shfl_sync(0xffffffffu, up, 8 * ti + 4);
 #pragma unroll
                 for (int s2 = 0; s2 < KS; ++s2) {
                     qb[s2][0] = pack_pair<PA_F16>(qv[4 * s2] * down, qv[4 * s2 + 1] * down);
@@ -847,10 +849,10 @@ __device__ __forceinline__ void decode_consumer_mma(const DecodeParams& p, uint8
                         }
                     }
                     // ---- online softmax: c0/c1 = token gi, heads 2ti/2ti+1; c2/c3 = token gi+8 ----
-                    const float s0 = v0 ? (sa[0] + sb[0]) * qk_scale : -INFINITY;
-                    const float s1 = v0 ? (sa[1] + sb[1]) * qk_scale : -INFINITY;
-                    const float s2 = v1 ? (sa[2] + sb[2]) * qk_scale : -INFINITY;
-                    const float s3 = v1 ? (sa[3] + sb[3]) * qk_scale : -INFINITY;
+                    const float s0 = v0 ? (sa[0] + sb[0]) * qk_scale0 : -INFINITY;
+                    const float s1 = v0 ? (sa[1] + sb[1]) * qk_scale1 : -INFINITY;
+                    const float s2 = v1 ? (sa[2] + sb[2]) * qk_scale0 : -INFINITY;
+                    const float s3 = v1 ? (sa[3] + sb[3]) * qk_scale1 : -INFINITY;
                     // The reference max of a head moves only when one of its
                     // scores passes it by more than tau; a lane tests its own
                     // four and the warp votes, so the reduction over the slice's
@@ -1344,7 +1346,9 @@ paged_decode_kernel(const DecodeParams p) {
         bool ok = __all_sync(0xffffffffu, mbar_wait(qfull0 + 8u * slot, (qn >> 1) & 1u, p.status, abort_flag));
         // this warp's queries as packed 16-bit pairs in the lane's chunk order
         uint32_t qw[C::GW][C::PL];
-        float qk_scale = p.qk_scale;
+        float qk_scale[C::GW];
+#pragma unroll
+        for (int g = 0; g < C::GW; ++g) qk_scale[g] = p.qk_scale;
         {
             const uint8_t* qs = qbuf + slot * QSLOT;
             if constexpr (C::KB == 2) {
@@ -1357,37 +1361,36 @@ paged_decode_kernel(const DecodeParams p) {
                             qw[g][(v * C::EV + e) / 2] = *reinterpret_cast<const uint32_t*>(
                                 qs + ((hg * C::GW + g) * D + (v * C::LPT + c) * C::EV + e) * C::QB);
             } else {
-                // E4M3 cache: queries to fp16, scaled by a power of two so that
-                // the largest lands in [2^14, 2^15) (exact but for components
-                // 2^28 times smaller than the largest); the scale is folded
-                // back into the score scale
-                float qv[C::GW][C::EPL];
-                float mx = 0.f;
+                // E4M3 cache: queries to fp16, a head's scaled by a power of two so
+                // that its largest lands in [2^14, 2^15) (exact but for components
+                // 2^28 times smaller than that one); the scale is folded back into
+                // the head's score scale
 #pragma unroll
-                for (int g = 0; g < C::GW; ++g)
+                for (int g = 0; g < C::GW; ++g) {
+                    float qv[C::EPL];
+                    float mx = 0.f;
 #pragma unroll
                     for (int v = 0; v < C::NV; ++v)
 #pragma unroll
                         for (int e = 0; e < C::EV; e += 2) {
                             const float2 f = kv_pair<QDT>(*reinterpret_cast<const uint32_t*>(
                                 qs + ((hg * C::GW + g) * D + (v * C::LPT + c) * C::EV + e) * C::QB));
-                            qv[g][v * C::EV + e] = f.x;
-                            qv[g][v * C::EV + e + 1] = f.y;
+                            qv[v * C::EV + e] = f.x;
+                            qv[v * C::EV + e + 1] = f.y;
                             mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
                         }
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                int ex = mx > 0.f ? ((__float_as_int(mx) >> 23) & 0xff) - 127 - 14 : 0;
-                ex = max(-100, min(100, ex));
-                const float down = __int_as_float((127 - ex) << 23), up = __int_as_float((127 + ex) << 23);
-                qk_scale *= up;
-#pragma unroll
-                for (int g = 0; g < C::GW; ++g)
+                    for (int o = 1; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    int ex = mx > 0.f ? ((__float_as_int(mx) >> 23) & 0xff) - 127 - 14 : 0;
+                    ex = max(-100, min(100, ex));
+                    const float down = __int_as_float((127 - ex) << 23), up = __int_as_float((127 + ex) << 23);
+                    qk_scale[g] *= up;
 #pragma unroll
                     for (int x = 0; x < C::PL; ++x) {
-                        const __half2 h = __floats2half2_rn(qv[g][2 * x] * down, qv[g][2 * x + 1] * down);
+                        const __half2 h = __floats2half2_rn(qv[2 * x] * down, qv[2 * x + 1] * down);
                         qw[g][x] = *reinterpret_cast<const uint32_t*>(&h);
                     }
+                }
             }
         }
         __syncwarp();
@@ -1484,7 +1487,7 @@ paged_decode_kernel(const DecodeParams p) {
 #pragma unroll
                         for (int h = 0; h < C::NB; ++h)
 #pragma unroll
-                            for (int g = 0; g < C::GW; ++g) sc[h][g] = (FULL || valid[h]) ? t[h][g] * qk_scale : -INFINITY;
+                            for (int g = 0; g < C::GW; ++g) sc[h][g] = (FULL || valid[h]) ? t[h][g] * qk_scale[g] : -INFINITY;
                     }
                     // ---- online softmax of this group over the NB steps, lazy rescale (warp-uniform test) ----
                     float smax[C::GW];
