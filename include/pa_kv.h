@@ -579,7 +579,7 @@ int32_t pa_pool_ref_count(void* pool, int64_t block);
 int32_t pa_pool_seq_len(void* pool, int64_t seq_id);
 
 /* ---------------------------------------------------------------------------
- * Test hook for the decode's wait timeout.  (Not on the pages: every wait of
+ * Test hooks for the wait timeouts.  (Not on the pages: every wait of
  * the library's kernels is bounded, so that a stalled copy ends in an error
  * status instead of a hung GPU.)
  *
@@ -590,12 +590,26 @@ int32_t pa_pool_seq_len(void* pool, int64_t seq_id);
  * kernel returns.  The output and workspace contents are unspecified
  * afterwards (within their stated sizes); the device stays usable.  For the
  * library's own tests; a serving path has no use for it.
+ * pa_decode_window_test_wait_timeout: the same of pa_decode_window, with its arguments.
+ * pa_prefill_test_wait_timeout: the same of pa_prefill_varlen_window (window > 0)
+ * or of the causal pa_prefill_varlen (window 0): its loader warps issue no copy.
  * ------------------------------------------------------------------------- */
 pa_status pa_decode_test_wait_timeout(void* out, const void* q, pa_dtype q_dtype, const pa_kv_cache* cache,
                                       const int32_t* block_table, int32_t max_blocks_per_seq,
                                       const int32_t* seq_lens, int32_t num_seqs, int32_t max_seq_len,
                                       int32_t num_heads, float scale, int32_t partition_size, void* workspace,
                                       size_t workspace_bytes, int32_t* dev_status, pa_stream_t stream);
+pa_status pa_decode_window_test_wait_timeout(void* out, const void* q, pa_dtype q_dtype, const pa_kv_cache* cache,
+                                             const int32_t* block_table, int32_t max_blocks_per_seq,
+                                             const int32_t* seq_lens, int32_t num_seqs, int32_t max_seq_len,
+                                             int32_t num_heads, float scale, int32_t window, int32_t num_sinks,
+                                             int32_t partition_size, void* workspace, size_t workspace_bytes,
+                                             int32_t* dev_status, pa_stream_t stream);
+pa_status pa_prefill_test_wait_timeout(void* out, const void* q, pa_dtype q_dtype, const pa_kv_cache* cache,
+                                       const int32_t* block_table, int32_t max_blocks_per_seq,
+                                       const int32_t* cu_seq_lens_q, const int32_t* cu_seq_lens_k, int32_t num_seqs,
+                                       int32_t max_seqlen_q, int32_t max_seqlen_k, int32_t num_heads, float scale,
+                                       int32_t window, int32_t num_sinks, int32_t* dev_status, pa_stream_t stream);
 
 #ifdef __cplusplus
 }

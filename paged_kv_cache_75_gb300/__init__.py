@@ -12,4 +12,5 @@ from ._binding import (  # noqa: F401
     pa_decode, pa_decode_append, pa_decode_cascade, pa_decode_cascade_workspace_size, pa_decode_partition_size, pa_decode_static_ws, pa_decode_test_wait_timeout, pa_prefill_varlen, pa_prefill_varlen_packed, pa_slot_mapping, pa_swap_blocks, pa_varlen_mixed, pa_varlen_mixed_workspace_size, torch_dtype_code,
     QKTransform, RopeFrequencies, rope_frequencies, pa_qk_norm_rope, pa_qk_norm_rope_write,
     pa_decode_window, pa_decode_window_workspace_size, pa_prefill_varlen_window,
+    pa_decode_window_test_wait_timeout, pa_prefill_test_wait_timeout,
 )

@@ -90,6 +90,10 @@ def library():
                                     C.c_int),
             "pa_decode_test_wait_timeout": ([vp, vp, C.c_int, pc, vp, i32, vp, i32, i32, i32, f32, i32, vp, sz, vp,
                                              vp], C.c_int),
+            "pa_decode_window_test_wait_timeout": ([vp, vp, C.c_int, pc, vp, i32, vp, i32, i32, i32, f32, i32, i32, i32, vp,
+                                                    sz, vp, vp], C.c_int),
+            "pa_prefill_test_wait_timeout": ([vp, vp, C.c_int, pc, vp, i32, vp, vp, i32, i32, i32, i32, f32, i32, i32, vp,
+                                              vp], C.c_int),
             "pa_decode_cascade_workspace_size": ([i32, i32, i32, i32, i32, i32], sz),
             "pa_decode_partition_size": ([i32, i32, i32, i32], i32),
             "pa_decode_cascade": ([vp, vp, C.c_int, pc, vp, i32, vp, i32, i32, i32, f32, vp, vp, i32, i32, i32,
@@ -447,6 +451,42 @@ def pa_decode_test_wait_timeout(out: torch.Tensor, q: torch.Tensor, cache: KVCac
                                                int(max_seq_len), H, float(scale), int(partition_size),
                                                _ptr(workspace), ws_bytes, _ptr(dev_status), _stream(q))
     _check(st, "pa_decode_test_wait_timeout")
+
+
+def pa_decode_window_test_wait_timeout(out: torch.Tensor, q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
+                                       seq_lens: torch.Tensor, max_seq_len: int, scale: float, window: int,
+                                       num_sinks: int = 0, partition_size: int = 0,
+                                       workspace: Optional[torch.Tensor] = None,
+                                       dev_status: Optional[torch.Tensor] = None):
+    """Test hook: pa_decode_window whose copies are never issued."""
+    _need(q, "q")
+    _need(out, "out", q.dtype)
+    B, H, D = q.shape
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    cs = cache.c_struct()
+    st = library().pa_decode_window_test_wait_timeout(_ptr(out), _ptr(q), torch_dtype_code(q.dtype), C.byref(cs),
+                                                      _ptr(block_table), block_table.shape[1], _ptr(seq_lens), B,
+                                                      int(max_seq_len), H, float(scale), int(window), int(num_sinks),
+                                                      int(partition_size), _ptr(workspace), ws_bytes, _ptr(dev_status),
+                                                      _stream(q))
+    _check(st, "pa_decode_window_test_wait_timeout")
+
+
+def pa_prefill_test_wait_timeout(out: torch.Tensor, q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
+                                 cu_seq_lens_q: torch.Tensor, cu_seq_lens_k: torch.Tensor, max_seqlen_q: int,
+                                 max_seqlen_k: int, scale: float, window: int = 0, num_sinks: int = 0,
+                                 dev_status: Optional[torch.Tensor] = None):
+    """Test hook: pa_prefill_varlen_window (window 0: the causal
+    pa_prefill_varlen) whose copies are never issued."""
+    _need(q, "q")
+    _need(out, "out", q.dtype)
+    cs = cache.c_struct()
+    st = library().pa_prefill_test_wait_timeout(_ptr(out), _ptr(q), torch_dtype_code(q.dtype), C.byref(cs),
+                                                _ptr(block_table), block_table.shape[1], _ptr(cu_seq_lens_q),
+                                                _ptr(cu_seq_lens_k), cu_seq_lens_q.shape[0] - 1, int(max_seqlen_q),
+                                                int(max_seqlen_k), q.shape[1], float(scale), int(window), int(num_sinks),
+                                                _ptr(dev_status), _stream(q))
+    _check(st, "pa_prefill_test_wait_timeout")
 
 
 def pa_decode_partition_size(num_seqs, num_heads, num_kv_heads, max_seq_len) -> int:

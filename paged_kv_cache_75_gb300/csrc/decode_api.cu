@@ -305,6 +305,21 @@ extern "C" pa_status pa_decode_test_wait_timeout(void* out, const void* q, pa_dt
                             stream, nullptr, nullptr, nullptr, nullptr, nullptr, 0, false, 0, true);
 }
 
+extern "C" pa_status pa_decode_window_test_wait_timeout(void* out, const void* q, pa_dtype q_dtype,
+                                                        const pa_kv_cache* cache, const int32_t* block_table,
+                                                        int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                                        int32_t num_seqs, int32_t max_seq_len, int32_t num_heads,
+                                                        float scale, int32_t window, int32_t num_sinks,
+                                                        int32_t partition_size, void* workspace,
+                                                        size_t workspace_bytes, int32_t* dev_status,
+                                                        pa_stream_t stream) {
+    if (window <= 0 || num_sinks < 0) return PA_ERR_INVALID_ARG;
+    return pa::decode_entry(out, q, q_dtype, cache, block_table, max_blocks_per_seq, seq_lens, num_seqs,
+                            max_seq_len, num_heads, scale, partition_size, workspace, workspace_bytes, dev_status,
+                            stream, nullptr, nullptr, nullptr, nullptr, nullptr, 0, false, 0, true, window,
+                            num_sinks);
+}
+
 extern "C" int32_t pa_decode_partition_size(int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads,
                                             int32_t max_seq_len) {
     if (num_seqs <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads != 0 || max_seq_len < 0)

@@ -105,7 +105,7 @@ struct DecodeParams {
     // head) that max_parts allows, so block i takes item i and no work list is
     // built (its sort takes 2.3 us, a third of a small batch's decode)
     int32_t one_round;
-    // test hook (pa_decode_test_wait_timeout; 0 on every other path): the
+    // test hooks (pa_decode*_test_wait_timeout; 0 on every other path): the
     // producer warp issues no copy at all, so every consumer wait runs out
     // with nothing in flight, reports PA_ERR_TIMEOUT and the block returns
     int32_t no_copies;

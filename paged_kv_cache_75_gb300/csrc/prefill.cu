@@ -97,7 +97,7 @@ constexpr int kMaxSeqs = 6144;                           // prefix of query tile
 
 struct PrefillParams {
     void* out;
-    const uint16_t* q;
+    const uint16_t* q;  // NULL (pa_prefill_test_wait_timeout): no copy is issued, every wait runs out
     const int32_t* block_table;
     const int32_t* cu_q;
     const int32_t* cu_k;
@@ -811,7 +811,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
         const CUtensorMap* map = kv == 0 ? &map_k : &map_v;
         const uint32_t nst = kv == 0 ? kStages : kStagesV;  // ring depth
         uint32_t fill = 0, stage = 0, phase = 0;
-        bool ok = true;
+        bool ok = p.q != nullptr;
         if constexpr (PACKED) {
             // a tile is 128 consecutive rows of one KV head: one 3-D box per
             // 64-column half (rows past the tensor read as zero; rows past the
@@ -912,7 +912,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
         // its rows past num_seqs * max_seqlen_q)
         const int64_t total_q = __ldg(p.cu_q + p.num_seqs);
         uint32_t qn = 0;
-        bool ok = true;
+        bool ok = p.q != nullptr;
         for (int rnd = 0, item; ok && (item = snake_item(rnd, n_items)) >= 0; ++rnd) {
             const Work w = item_work(rnd, item);
             if (w.ntiles == 0) continue;
@@ -1515,12 +1515,13 @@ using namespace pa;
 namespace pa {
 namespace {
 
-// pa_prefill_varlen, and pa_prefill_varlen_window when window > 0
+// pa_prefill_varlen, and pa_prefill_varlen_window when window > 0; no_copies: the
+// test hook's launch
 pa_status prefill_entry(void* out, const void* q, pa_dtype q_dtype, const pa_kv_cache* cache,
                         const int32_t* block_table, int32_t max_blocks_per_seq, const int32_t* cu_seq_lens_q,
                         const int32_t* cu_seq_lens_k, int32_t num_seqs, int32_t max_seqlen_q, int32_t max_seqlen_k,
                         int32_t num_heads, float scale, int32_t causal, int32_t window, int32_t sinks,
-                        int32_t* dev_status, pa_stream_t stream) {
+                        int32_t* dev_status, pa_stream_t stream, bool no_copies = false) {
     pa_status st = check_cache(cache);
     if (st != PA_OK) return st;
     if (num_seqs < 0 || num_heads <= 0 || max_blocks_per_seq <= 0 || max_seqlen_q < 0 ||
@@ -1572,6 +1573,7 @@ pa_status prefill_entry(void* out, const void* q, pa_dtype q_dtype, const pa_kv_
     CUtensorMap map_q;
     if (!make_q_map(&map_q, q, num_heads, group, num_seqs, max_seqlen_q, q_dtype)) return PA_ERR_CUDA;
     p.q_rows = q_map_rows(num_seqs, max_seqlen_q);
+    if (no_copies) p.q = nullptr;
     if (window > 0) {
         // (a window, or sinks, past the longest sequence change nothing more)
         const int32_t most = max_seqlen_k > 1 ? max_seqlen_k : 1;
@@ -1609,6 +1611,18 @@ extern "C" pa_status pa_prefill_varlen_window(void* out, const void* q, pa_dtype
     return pa::prefill_entry(out, q, q_dtype, cache, block_table, max_blocks_per_seq, cu_seq_lens_q, cu_seq_lens_k,
                              num_seqs, max_seqlen_q, max_seqlen_k, num_heads, scale, 1, window, num_sinks, dev_status,
                              stream);
+}
+
+extern "C" pa_status pa_prefill_test_wait_timeout(void* out, const void* q, pa_dtype q_dtype, const pa_kv_cache* cache,
+                                                  const int32_t* block_table, int32_t max_blocks_per_seq,
+                                                  const int32_t* cu_seq_lens_q, const int32_t* cu_seq_lens_k,
+                                                  int32_t num_seqs, int32_t max_seqlen_q, int32_t max_seqlen_k,
+                                                  int32_t num_heads, float scale, int32_t window, int32_t num_sinks,
+                                                  int32_t* dev_status, pa_stream_t stream) {
+    if (window < 0 || num_sinks < 0 || !(scale > 0.f) || !std::isfinite(scale)) return PA_ERR_INVALID_ARG;
+    return pa::prefill_entry(out, q, q_dtype, cache, block_table, max_blocks_per_seq, cu_seq_lens_q, cu_seq_lens_k,
+                             num_seqs, max_seqlen_q, max_seqlen_k, num_heads, scale, 1, window, num_sinks, dev_status,
+                             stream, true);
 }
 
 extern "C" pa_status pa_prefill_varlen_packed(void* out, const void* q, const void* k, const void* v,
