@@ -53,7 +53,7 @@ typedef enum {
     PA_OK = 0,
     PA_ERR_INVALID_ARG = 1,  /* bad pointer, size, shape or length */
     PA_ERR_UNSUPPORTED = 2,  /* valid, but a head size / dtype / block size not built */
-    PA_ERR_OOM = 3,          /* the block pool has too few free blocks */
+    PA_ERR_OOM = 3,          /* the block pool has too few free blocks, or the host no memory */
     PA_ERR_CUDA = 4,         /* a CUDA launch or query failed */
     PA_ERR_TIMEOUT = 5,      /* device: a bounded wait ran out (dev_status only) */
     PA_ERR_BAD_BLOCK = 6     /* device: block id or slot outside the cache */

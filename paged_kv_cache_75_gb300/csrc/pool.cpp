@@ -18,10 +18,14 @@
 // Choices where the pages leave room: an append that cannot get all of its
 // blocks changes nothing (the page's sketch raises part-way through); the
 // copy-on-write block is taken before the blocks for new tokens.
+//
+// No exception leaves an entry: what a call allocates it allocates before it
+// changes anything, and PA_ERR_OOM is all that a lack of host memory does.  (The free
+// list is a ring of num_blocks ids for that: giving a block back allocates nothing.)
 #include <cstdint>
-#include <deque>
 #include <new>
 #include <unordered_map>
+#include <utility>
 #include <vector>
 
 #include "pa_kv.h"
@@ -37,15 +41,24 @@ struct Sequence {
 struct Pool {
     int64_t num_blocks = 0;
     int32_t block_size = 0;
-    std::deque<int32_t> free_list;
+    std::vector<int32_t> free_ring;       // the free list: `num_free` ids from `head` on, wrapping
+    int64_t head = 0, num_free = 0;
     std::vector<int32_t> ref;
     std::unordered_map<int64_t, Sequence> seqs;
 
     int32_t take() {
-        int32_t b = free_list.front();
-        free_list.pop_front();
+        int32_t b = free_ring[head];
+        head = head + 1 == num_blocks ? 0 : head + 1;
+        --num_free;
         ref[b] = 1;
         return b;
+    }
+    // one reference less; the last one gives the block back
+    void drop(int32_t b) {
+        if (--ref[b] > 0) return;
+        const int64_t at = head + num_free;
+        free_ring[at < num_blocks ? at : at - num_blocks] = b;
+        ++num_free;
     }
 };
 
@@ -63,20 +76,26 @@ pa_status pa_pool_create(int64_t num_blocks, int32_t block_size, const int32_t* 
     if (p == nullptr) return PA_ERR_OOM;
     p->num_blocks = num_blocks;
     p->block_size = block_size;
-    p->ref.assign(static_cast<size_t>(num_blocks), 0);
-    if (free_order != nullptr) {
-        std::vector<char> seen(static_cast<size_t>(num_blocks), 0);
-        for (int64_t i = 0; i < num_blocks; ++i) {
-            int32_t b = free_order[i];
+    p->num_free = num_blocks;
+    std::vector<char> seen;
+    try {
+        p->ref.assign(static_cast<size_t>(num_blocks), 0);
+        p->free_ring.resize(static_cast<size_t>(num_blocks));
+        if (free_order != nullptr) seen.assign(static_cast<size_t>(num_blocks), 0);
+    } catch (const std::bad_alloc&) {
+        delete p;
+        return PA_ERR_OOM;
+    }
+    for (int64_t i = 0; i < num_blocks; ++i) {
+        const int32_t b = free_order != nullptr ? free_order[i] : static_cast<int32_t>(i);
+        if (free_order != nullptr) {
             if (b < 0 || b >= num_blocks || seen[b]) {
                 delete p;
                 return PA_ERR_INVALID_ARG;  // not a permutation
             }
             seen[b] = 1;
-            p->free_list.push_back(b);
         }
-    } else {
-        for (int64_t i = 0; i < num_blocks; ++i) p->free_list.push_back(static_cast<int32_t>(i));
+        p->free_ring[i] = b;
     }
     *pool_out = p;
     return PA_OK;
@@ -87,7 +106,11 @@ void pa_pool_destroy(void* pool) { delete as_pool(pool); }
 pa_status pa_pool_add_seq(void* pool, int64_t seq_id) {
     Pool* p = as_pool(pool);
     if (p == nullptr || p->seqs.count(seq_id)) return PA_ERR_INVALID_ARG;
-    p->seqs.emplace(seq_id, Sequence());
+    try {
+        p->seqs.emplace(seq_id, Sequence());
+    } catch (const std::bad_alloc&) {
+        return PA_ERR_OOM;
+    }
     return PA_OK;
 }
 
@@ -108,8 +131,15 @@ pa_status pa_pool_append(void* pool, int64_t seq_id, int32_t n_tokens, int64_t* 
     const int64_t blocks_after = (s.length + n_tokens + bs - 1) / bs;
     const int64_t new_blocks = blocks_after - static_cast<int64_t>(s.blocks.size());
     const bool cow = (s.length % bs) != 0 && p->ref[s.blocks.back()] > 1;
-    if (new_blocks + (cow ? 1 : 0) > static_cast<int64_t>(p->free_list.size())) return PA_ERR_OOM;
+    if (new_blocks + (cow ? 1 : 0) > p->num_free) return PA_ERR_OOM;
     if (cow && (cow_pairs_out == nullptr || n_cow_out == nullptr)) return PA_ERR_INVALID_ARG;
+    try {
+        // (doubling, as appends of a token at a time need)
+        const size_t need = static_cast<size_t>(blocks_after);
+        if (need > s.blocks.capacity()) s.blocks.reserve(need > 2 * s.blocks.capacity() ? need : 2 * s.blocks.capacity());
+    } catch (const std::bad_alloc&) {
+        return PA_ERR_OOM;
+    }
 
     if (cow) {
         int32_t old_b = s.blocks.back();
@@ -135,10 +165,15 @@ pa_status pa_pool_fork(void* pool, int64_t parent, int64_t child) {
     if (p == nullptr || p->seqs.count(child)) return PA_ERR_INVALID_ARG;
     auto it = p->seqs.find(parent);
     if (it == p->seqs.end()) return PA_ERR_INVALID_ARG;
-    Sequence copy = it->second;
-    for (int32_t b : copy.blocks)
+    const Sequence* held;
+    try {
+        Sequence copy = it->second;
+        held = &p->seqs.emplace(child, std::move(copy)).first->second;
+    } catch (const std::bad_alloc&) {
+        return PA_ERR_OOM;
+    }
+    for (int32_t b : held->blocks)
         if (b >= 0) p->ref[b] += 1;
-    p->seqs.emplace(child, std::move(copy));
     return PA_OK;
 }
 
@@ -147,11 +182,8 @@ pa_status pa_pool_free_seq(void* pool, int64_t seq_id) {
     if (p == nullptr) return PA_ERR_INVALID_ARG;
     auto it = p->seqs.find(seq_id);
     if (it == p->seqs.end()) return PA_ERR_INVALID_ARG;
-    for (int32_t b : it->second.blocks) {
-        if (b < 0) continue;
-        p->ref[b] -= 1;
-        if (p->ref[b] == 0) p->free_list.push_back(b);
-    }
+    for (int32_t b : it->second.blocks)
+        if (b >= 0) p->drop(b);
     p->seqs.erase(it);
     return PA_OK;
 }
@@ -177,15 +209,7 @@ pa_status pa_pool_release_window(void* pool, int64_t seq_id, int32_t window, int
         if (j >= end) break;
         const int32_t b = s.blocks[j];
         if (b < 0) continue;
-        if (p->ref[b] == 1) {
-            try {
-                p->free_list.push_back(b);
-            } catch (const std::bad_alloc&) {
-                if (n_released_out) *n_released_out = n;
-                return PA_ERR_OOM;  // the blocks so far are released, the others as they were
-            }
-        }
-        p->ref[b] -= 1;
+        p->drop(b);
         s.blocks[j] = -1;
         ++n;
     }
@@ -218,7 +242,7 @@ pa_status pa_pool_block_table(void* pool, const int64_t* seq_ids, int32_t n, int
 
 int64_t pa_pool_num_free(void* pool) {
     Pool* p = as_pool(pool);
-    return p ? static_cast<int64_t>(p->free_list.size()) : -1;
+    return p ? p->num_free : -1;
 }
 
 int32_t pa_pool_ref_count(void* pool, int64_t block) {
