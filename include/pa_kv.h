@@ -105,7 +105,8 @@ int32_t pa_version(void);
  * A 16-bit cache must have kv_dtype == in_dtype: the bits are moved
  *   unchanged.  An E4M3 cache stores e4m3_satfinite(round-to-nearest-even(
  *   (float)x / scale)), the division done in IEEE binary32.
- * Several tokens with the same slot: which one lands is unspecified.
+ * Several tokens with the same slot: which one's elements land is unspecified (a
+ * mixture of theirs is possible).
  * ------------------------------------------------------------------------- */
 pa_status pa_kv_cache_write(const pa_kv_cache* cache, const void* k, const void* v,
                             pa_dtype in_dtype, int64_t num_tokens, int64_t token_stride,
@@ -317,6 +318,12 @@ pa_status pa_decode_static_ws(void* out, const void* q, pa_dtype q_dtype, const 
  * then the window's); 0 cuts them into equal parts that fill the GPU, of 128
  * tokens or more.  workspace: pa_decode_window_workspace_size
  * (...) bytes with the same arguments.  Everything else as pa_decode.
+ * Rounding (pa_decode's too): scores, maxima, sums and outputs are binary32 up to the one
+ * rounding of out, with these exceptions.  With num_heads / num_kv_heads of 4 or 8 a
+ * weight meets its value in 16 bits on the tensor cores: fp16 and E4M3 caches as fp16
+ * (off by 2^-11 of itself, below 2^-14 of the largest by 2^-25 of that), bf16 caches as
+ * two bf16 parts (2^-16).  Over an E4M3 cache a head's query is taken in fp16 relative to
+ * its largest component: exact but for components 2^28 times smaller.
  * ------------------------------------------------------------------------- */
 size_t pa_decode_window_workspace_size(int32_t num_seqs, int32_t num_heads, int32_t head_size, int32_t max_seq_len,
                                        int32_t block_size, int32_t window, int32_t num_sinks,
@@ -340,7 +347,8 @@ pa_status pa_decode_window(void* out, const void* q, pa_dtype q_dtype, const pa_
  * be in the cache, e.g. by pa_kv_cache_write).  With Lq query rows, query i
  * sits at position Lk - Lq + i; with causal != 0 it sees keys j <= Lk - Lq + i
  * (bottom-right alignment), otherwise all Lk keys.  A row that sees no key
- * outputs 0.
+ * outputs 0.  A value that some query of a sequence sees must be finite for the
+ * sequence's other queries too (a weight of zero still multiplies it).
  * q, out: device [total_q][num_heads][head_size] of q_dtype (BF16 or F16,
  *   equal to kv_dtype), total_q = cu_seq_lens_q[num_seqs], 16-byte aligned.
  * cu_seq_lens_q, cu_seq_lens_k: device int32 [num_seqs + 1], non-decreasing,
@@ -370,6 +378,9 @@ pa_status pa_prefill_varlen(void* out, const void* q, pa_dtype q_dtype, const pa
  * or NaN, and also where other queries see it).  A value that is not finite and that
  * a query sees costs time: the rows that share its tiles are worked out one by one.
  * scale > 0.  Everything else as pa_prefill_varlen (head_size 128).
+ * Rounding (pa_prefill_varlen's too): scores, maxima, sums and outputs are binary32 up to
+ * the one rounding of out; a weight meets its value in 16 bits on the tensor cores, as
+ * fp16 (off by 2^-11 of itself) or, with bf16 caches, as two bf16 parts (2^-16).
  * ------------------------------------------------------------------------- */
 pa_status pa_prefill_varlen_window(void* out, const void* q, pa_dtype q_dtype, const pa_kv_cache* cache,
                                    const int32_t* block_table, int32_t max_blocks_per_seq,

@@ -70,13 +70,16 @@ int window_most_parts(int64_t num_seqs, int tokens) {
 // their n equal parts fill the c resident blocks: rounds of all blocks share the
 // memory's rate, the last round's blocks run at a block's own rate when they are
 // few, every round costs an item's start and end, parts cost a merge.  The n with
-// the least such time is taken (of equal ones, to 2 %, the larger).  Measured
-// against it: 16 sequences of 8 KV heads, window 4096, bf16: 3 parts 51 us, 1 part 78,
-// 4 parts (a second, nearly empty round) 72; 64 such sequences: 4 parts 175, 1 part
-// 210; 24: 2 parts 70, 1 part 87, 3 parts 97; 8 E4M3 sequences, window 8192: 6 parts 33, the
-// plain rule's 17 parts 45; one sequence, window 4096: 29 parts 14.4, 9 parts 17.8.
+// the least such time is taken (of equal ones, to 2 %, the larger).  Measured, its
+// choice first: 16 sequences of 8 KV heads of 128, window 4096, bf16: 3 parts 49 us, 1 part 76,
+// 4 parts (a second, nearly empty round) 72; 64 such sequences: 6 parts 176, 4 parts
+// 175, 1 part 210; 24: 2 parts 68, 1 part 85, 3 parts 95; 8 E4M3 sequences, window 8192: 7 parts
+// 33, 6 parts 31, the plain rule's 17 parts 46; one sequence, window 4096: 33 parts 11.3, 9
+// parts 15.8.  (Registers and shared memory hold the kernels to three blocks an SM; some
+// of head size 64 fit four, which moves little: 16 sequences of 8 KV heads of 64, window
+// 4096: the model's 3 parts 29.5, 4 parts 28.8.)
 int window_partition(int64_t num_seqs, int num_kv_heads, int tokens, int block_size, int token_bytes) {
-    const double c = 3.0 * device_sm_count();  // resident decode blocks
+    const double c = 3.0 * device_sm_count();  // resident blocks
     const double memory = 6.7e6, block = 28e3;  // bytes a microsecond: all blocks, one block
     const double item = 2.5, merge = 3.0;       // microseconds: an item's start and end, a merge launch
     const double pairs = static_cast<double>(num_seqs) * num_kv_heads;

@@ -44,13 +44,15 @@
 //
 // Sliding window and sinks (pa_prefill_varlen_window): an item works on the
 // sinks' blocks and those of its window as if they were all of its keys, so its
-// tiles hold few keys that no row sees (1028 of 1168 on average for a window of
-// 1024, 32 queries, blocks of 16).  Bound by the softmax warps' chain of about 2300
-// cycles a tile (the MMA warp issues about 2000 beside it: bf16 weights take two PV
-// passes) and some 5000 cycles an item: its first tile's true maximum, the
-// previous item's output.  On one GB300 eight chunks of 512 to 2048 queries on up
-// to 4096 cached tokens (32/8 heads, bf16, window 1024, 4 sinks) take 222 us, 682
-// TFLOP/s of visible pairs; one prompt of 8192 tokens, window 2048, 276 us, 878 TFLOP/s.
+// tiles hold few keys that no row sees (1028 seen of 1152 for an item past the
+// window's start: a window of 1024, 4 sinks, 32 queries, blocks of 16).  Bound by the
+// softmax warps' chain of about 2330 cycles a tile (scores 240, exponentials and vote
+// 1100, weights stored 580; beside it the issuing thread spends 970 on PV, two passes
+// of bf16 weights, and 390 on QK) and some 5000 cycles an item: its first tile's true
+// maximum (1860), the previous item's output.  On one GB300 eight chunks of 512 to
+// 2048 queries on up to 4096 cached tokens (32/8 heads, bf16, window 1024, 4 sinks) take
+// 223 us, 679 TFLOP/s of visible pairs; one prompt of 8192 tokens, window 2048, 280 us,
+// 866 TFLOP/s; in fp16, one PV pass, 196 and 243 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

@@ -146,8 +146,8 @@ __device__ __forceinline__ uint64_t widen(uint32_t w) {
 
 // 8 values (packed pairs) -> 8 E4M3 codes: IEEE division, then one rounding with
 // saturation.  (By a power of two, x / scale and x * (1 / scale) are the same
-// number rounded once; 16 divisions a lane cost a batch of 256 tokens a
-// quarter of its 5.1 us.)
+// number rounded once.  16 divisions a lane by other scales: 256 tokens, 32/8 heads,
+// 5.0 us for 3.9; 16384 tokens, normed, 83 us for 67.)
 __device__ __forceinline__ uint2 e4m3_8(const uint64_t* x, float scale, float inverse) {
     uint32_t c[4];
 #pragma unroll
