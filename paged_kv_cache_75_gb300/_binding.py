@@ -156,6 +156,11 @@ def _native():
     return _native_mod
 
 
+def _clamp32(x) -> int:
+    """A window or a count as the 32-bit argument that means the same (ctypes would take the low bits)."""
+    return max(-1, min(int(x), 2 ** 31 - 1))
+
+
 def _need(t, name, dtype=None, cuda=True):
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a tensor" % name)
@@ -421,7 +426,7 @@ def pa_decode(out: torch.Tensor, q: torch.Tensor, cache: KVCache, block_table: t
 def pa_decode_window_workspace_size(num_seqs, num_heads, head_size, max_seq_len, block_size, window, num_sinks=0,
                                     partition_size=0) -> int:
     return int(library().pa_decode_window_workspace_size(num_seqs, num_heads, head_size, int(max_seq_len), block_size,
-                                                         int(window), int(num_sinks), int(partition_size)))
+                                                         _clamp32(window), _clamp32(num_sinks), int(partition_size)))
 
 
 def pa_decode_window(out: torch.Tensor, q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
@@ -658,7 +663,7 @@ class BlockPool:
         """Gives back the blocks that no query from the sequence's last position
         on sees; returns how many."""
         n = C.c_int32(0)
-        _check(library().pa_pool_release_window(self._h, seq_id, window, num_sinks, C.byref(n)),
+        _check(library().pa_pool_release_window(self._h, seq_id, _clamp32(window), _clamp32(num_sinks), C.byref(n)),
                "pa_pool_release_window")
         return n.value
 

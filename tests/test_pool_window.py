@@ -133,3 +133,24 @@ def test_random_operations_against_the_model(seed):
             assert t == [table(m, s, width) for s in m.seqs]
             assert lens == [m.seqs[s][1] for s in m.seqs]
         assert [pool.ref_count(b) for b in range(nb)] == m.ref
+
+
+def test_windows_past_32_bits_mean_everything():
+    """A window or a sink count that no 32-bit argument holds is the largest one, not its low bits."""
+    pkg_build.build()
+    p = pk.BlockPool(64, 4)
+    p.add_seq(1)
+    p.append(1, 200)
+    free = p.num_free()
+    for window in (2 ** 31 - 1, 2 ** 31, 2 ** 32 + 5, 2 ** 63 + 5):
+        assert p.release_window(1, window) == 0 and p.num_free() == free
+    for sinks in (2 ** 31 - 1, 2 ** 32, 2 ** 64 + 3):
+        assert p.release_window(1, 8, sinks) == 0
+    for window, sinks in ((0, 0), (-1, 0), (5 - 2 ** 32, 0), (8, -1), (8, 5 - 2 ** 32)):
+        with pytest.raises(pk.PaError):
+            p.release_window(1, window, sinks)
+    size = pk.pa_decode_window_workspace_size
+    assert size(4, 8, 128, 300, 16, 2 ** 32 + 5, 0, 64) == size(4, 8, 128, 300, 16, 2 ** 31 - 1, 0, 64) > 0
+    assert size(4, 8, 128, 300, 16, 5 - 2 ** 32, 0, 64) == 0
+    assert size(4, 8, 128, 300, 16, 8, 2 ** 40, 64) == size(4, 8, 128, 300, 16, 8, 300, 64)
+    assert p.release_window(1, 8) > 0
