@@ -62,7 +62,8 @@ typedef enum {
 typedef enum {
     PA_F16 = 0,       /* IEEE binary16 */
     PA_BF16 = 1,      /* bfloat16 */
-    PA_FP8_E4M3 = 2   /* OCP FP8 E4M3 (finite-only "fn"), KV cache only */
+    PA_FP8_E4M3 = 2,  /* OCP FP8 E4M3 (finite-only "fn"), KV cache only */
+    PA_F32 = 3        /* IEEE binary32, logits only (pa_beam_select) */
 } pa_dtype;
 
 /* Description of one layer's paged KV cache (device memory owned by the
@@ -477,6 +478,80 @@ pa_status pa_decode_cascade(void* out, const void* q, pa_dtype q_dtype, const pa
                             void* workspace, size_t workspace_bytes, int32_t* dev_status, pa_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Beam search: selection.  ("Как работает paged attention? (детально)" 3.3 and the
+ * vLLM paper summary name beam search among what shares blocks; its step is a selection,
+ * then a reordering of the beams' states.)
+ *
+ * For the rows r = cu_beams[b] .. cu_beams[b+1]-1 (the beams of request b) with scores
+ * c_r (sums of log-probabilities so far) and logits x_ri over the allowed tokens A_r:
+ *     s(r, i) = c_r + (x_ri - log sum_{j in A_r} exp(x_rj)),   i in A_r
+ * The request's num_select largest, in descending order, ties to the lower row, then
+ * the lower token: scores_out, rows_out (r, a row of logits), tokens_out (i), each device
+ * [num_requests][num_select]; past the candidates there are -inf, -1, -1.  s is computed
+ * beyond binary32 (its logarithm's sum to about 2^-27) and ordered so; scores_out is it rounded
+ * once.
+ *
+ * logits: device, [num_rows][vocab] of dtype (F16, BF16 or F32), rows row_stride >=
+ *   vocab elements apart, any alignment that the type has (16-byte aligned rows go
+ *   faster).  A logit of -inf is no candidate.  An allowed logit that is NaN or +inf is
+ *   reported as PA_ERR_INVALID_ARG and its row offers nothing.
+ * scores: device float [num_rows].  -inf: the row offers nothing (a beam that a request
+ *   does not have yet).  NaN or +inf is reported, the row offers nothing.
+ * cu_beams: device int32 [num_requests + 1], non-decreasing, within 0 .. num_rows (a request
+ *   that breaks this is reported and gets no candidates).
+ * allowed: device bit masks [num_rows][ceil(vocab/32)] uint32, bit i % 32 of word i / 32
+ *   set where token i is allowed, rows allowed_stride words apart; NULL: every
+ *   token.  Logits that are not allowed may hold anything.
+ * ended: device uint8 [num_rows], nullable: a row != 0 has one candidate, (r, end_token)
+ *   with s = c_r; its logits are not read.
+ * workspace: pa_beam_select_workspace_size(...) bytes, 16-byte aligned.
+ * Supported: num_select <= 64.
+ * ------------------------------------------------------------------------- */
+size_t pa_beam_select_workspace_size(int32_t num_rows, int32_t vocab, int32_t num_select);
+pa_status pa_beam_select(float* scores_out, int32_t* rows_out, int32_t* tokens_out, const void* logits,
+                         pa_dtype dtype, int64_t row_stride, int32_t vocab, int32_t num_rows, const float* scores,
+                         const int32_t* cu_beams, int32_t num_requests, const uint32_t* allowed,
+                         int64_t allowed_stride, const uint8_t* ended, int32_t end_token, int32_t num_select,
+                         void* workspace, size_t workspace_bytes, int32_t* dev_status, pa_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Beam search: reordering ("Как работает paged attention?" 3.3: beams refer to the same
+ * blocks; a shared block is copied before a sequence writes into it).
+ *
+ * New row i goes on from row p = parents[i] of the old tables with one more token, at
+ * position L = seq_lens[p]:
+ *   block_table_out[i] is block_table[p]'s first ceil(L / block_size) entries, -1 behind;
+ *   where L % block_size == 0, entry L / block_size is spare_blocks[i];
+ *   otherwise the first row (lowest i) with this parent keeps the parent's partly
+ *   filled block, and each other one has spare_blocks[i] there, to which the block's
+ *   first L % block_size token rows are copied (all KV heads, K and V, every layer);
+ *   seq_lens_out[i] = L + 1, slot_mapping_out[i] is position L's slot (for
+ *   pa_kv_cache_write of the new token), spare_used_out[i] tells whether
+ *   spare_blocks[i] went into the table.
+ * parents[i] < 0: an empty row (-1 everywhere, length 0, slot -1).
+ * So the partly filled block must be its row's alone (which these rules keep up: a
+ *   beam's own last block is never shared); whole blocks are shared freely.
+ *
+ * caches: host array of num_layers caches of one shape and type, which the tables serve.
+ * parents, spare_blocks, seq_lens_out, spare_used_out: device int32 [num_rows];
+ * slot_mapping_out: device int64 [num_rows]; block_table, block_table_out: device int32
+ * [num_rows_in], [num_rows] rows of max_blocks_per_seq; seq_lens: device int32
+ * [num_rows_in].  The old tables and the new are different memory.
+ * Reported in *dev_status: a parent past num_rows_in or a length outside 0 ..
+ *   max_blocks_per_seq * block_size - 1 (PA_ERR_INVALID_ARG; the row is empty), a block
+ *   that position L needs outside the cache (PA_ERR_BAD_BLOCK; its entry and slot are -1,
+ *   nothing is copied).
+ * pa_pool_reserve / pa_pool_reorder / pa_pool_unreserve are the host's side: spare
+ *   blocks are reserved ahead, the device goes on without waiting for the host, and the pool
+ *   follows by the same rule once the parents are known there.
+ * ------------------------------------------------------------------------- */
+pa_status pa_beam_reorder(const pa_kv_cache* caches, int32_t num_layers, const int32_t* parents, int32_t num_rows,
+                          const int32_t* block_table, int32_t num_rows_in, int32_t max_blocks_per_seq,
+                          const int32_t* seq_lens, const int32_t* spare_blocks, int32_t* block_table_out,
+                          int32_t* seq_lens_out, int64_t* slot_mapping_out, int32_t* spare_used_out,
+                          int32_t* dev_status, pa_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Mixed batch dispatcher: a varlen batch (as pa_prefill_varlen) whose
  * trailing sequences have one query token each is split -- the leading
  * sequences go to the varlen tensor-core kernel, the trailing one-token run
@@ -570,6 +645,19 @@ pa_status pa_slot_mapping(const int32_t* block_table, int32_t num_seqs, int32_t 
  *   holes over; pa_decode and the other unwindowed calls report them as
  *   PA_ERR_BAD_BLOCK).  *n_released_out (nullable): how many.  window >= 1,
  *   num_sinks >= 0.
+ * pa_pool_reserve(n): the next n blocks of the free list (reference count 1) become the
+ *   caller's own, of no sequence, until pa_pool_reorder gives them to one or
+ *   pa_pool_unreserve returns them (to the tail, in the order given; an id that is not
+ *   reserved, or twice, gives PA_ERR_INVALID_ARG and changes nothing).
+ * pa_pool_reorder: what pa_beam_reorder does, in the pool.  The sequences new_ids[i] take
+ *   the place of the sequences old_ids (all of them end): new_ids[i] goes on from old_ids
+ *   [parents[i]] with one token more, by pa_beam_reorder's rules with spare_blocks
+ *   (reserved ids; those used stop being reserved, the others stay the caller's).
+ *   parents[i] < 0: an empty sequence.  slots_out, spare_used_out: host [num_new],
+ *   nullable.  Ids are distinct among the old and among the new; a new id is an old one or
+ *   unknown.  A parent whose partly filled block another sequence holds too, a spare
+ *   that is needed and not reserved (or named twice), or bad ids give PA_ERR_INVALID_ARG
+ *   and change nothing.
  * Sequence ids are arbitrary int64 keys; an unknown id gives
  * PA_ERR_INVALID_ARG.
  * ------------------------------------------------------------------------- */
@@ -583,6 +671,11 @@ pa_status pa_pool_fork(void* pool, int64_t parent, int64_t child);
 pa_status pa_pool_free_seq(void* pool, int64_t seq_id);
 pa_status pa_pool_release_window(void* pool, int64_t seq_id, int32_t window, int32_t num_sinks,
                                  int32_t* n_released_out);
+pa_status pa_pool_reserve(void* pool, int32_t n, int32_t* blocks_out);
+pa_status pa_pool_unreserve(void* pool, const int32_t* blocks, int32_t n);
+pa_status pa_pool_reorder(void* pool, const int64_t* old_ids, int32_t num_old, const int64_t* new_ids, int32_t num_new,
+                          const int32_t* parents, const int32_t* spare_blocks, int64_t* slots_out,
+                          int32_t* spare_used_out);
 pa_status pa_pool_block_table(void* pool, const int64_t* seq_ids, int32_t n, int32_t max_blocks,
                               int32_t* table_out, int32_t* lens_out);
 int64_t pa_pool_num_free(void* pool);

@@ -6,7 +6,7 @@ from typing import Optional
 
 import torch
 
-PA_F16, PA_BF16, PA_FP8_E4M3 = 0, 1, 2
+PA_F16, PA_BF16, PA_FP8_E4M3, PA_F32 = 0, 1, 2, 3
 _TORCH_CODE = {torch.float16: PA_F16, torch.bfloat16: PA_BF16, torch.float8_e4m3fn: PA_FP8_E4M3}
 
 library_path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libpa_kv.so")
@@ -73,6 +73,9 @@ def library():
             "pa_pool_fork": ([vp, i64, i64], C.c_int),
             "pa_pool_free_seq": ([vp, i64], C.c_int),
             "pa_pool_release_window": ([vp, i64, i32, i32, C.POINTER(i32)], C.c_int),
+            "pa_pool_reserve": ([vp, i32, vp], C.c_int),
+            "pa_pool_unreserve": ([vp, vp, i32], C.c_int),
+            "pa_pool_reorder": ([vp, vp, i32, vp, i32, vp, vp, vp, vp], C.c_int),
             "pa_pool_block_table": ([vp, vp, i32, i32, vp, vp], C.c_int),
             "pa_pool_num_free": ([vp], i64),
             "pa_pool_ref_count": ([vp, i64], i32),
@@ -94,6 +97,10 @@ def library():
                                                     sz, vp, vp], C.c_int),
             "pa_prefill_test_wait_timeout": ([vp, vp, C.c_int, pc, vp, i32, vp, vp, i32, i32, i32, i32, f32, i32, i32, vp,
                                               vp], C.c_int),
+            "pa_beam_select_workspace_size": ([i32, i32, i32], sz),
+            "pa_beam_select": ([vp, vp, vp, vp, C.c_int, i64, i32, i32, vp, vp, i32, vp, i64, vp, i32, i32, vp, sz, vp,
+                                vp], C.c_int),
+            "pa_beam_reorder": ([pc, i32, vp, i32, vp, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp], C.c_int),
             "pa_decode_cascade_workspace_size": ([i32, i32, i32, i32, i32, i32], sz),
             "pa_decode_partition_size": ([i32, i32, i32, i32], i32),
             "pa_decode_cascade": ([vp, vp, C.c_int, pc, vp, i32, vp, i32, i32, i32, f32, vp, vp, i32, i32, i32,
@@ -610,6 +617,129 @@ def pa_prefill_varlen_window(out: torch.Tensor, q: torch.Tensor, cache: KVCache,
                                            window, num_sinks, dev_status), "pa_prefill_varlen_window")
 
 
+_LOGITS_CODE = {torch.float16: PA_F16, torch.bfloat16: PA_BF16, torch.float32: PA_F32}
+
+
+def _beside(t, name, like, dtype, shape):
+    """A contiguous CUDA tensor of that type and shape on `like`'s device."""
+    _need(t, name, dtype)
+    if t.device != like.device:
+        raise ValueError("%s must be on %s" % (name, like.device))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must be %s" % (name, list(shape)))
+
+
+def _status_beside(t, like):
+    if t is not None:
+        _beside(t, "dev_status", like, torch.int32, t.shape)
+        if t.numel() < 1:
+            raise ValueError("dev_status must have an entry")
+
+
+def pa_beam_select_workspace_size(num_rows, vocab, num_select) -> int:
+    return int(library().pa_beam_select_workspace_size(int(num_rows), int(vocab), int(num_select)))
+
+
+def pa_beam_select(scores_out: torch.Tensor, rows_out: torch.Tensor, tokens_out: torch.Tensor, logits: torch.Tensor,
+                   scores: torch.Tensor, cu_beams: torch.Tensor, allowed: Optional[torch.Tensor] = None,
+                   ended: Optional[torch.Tensor] = None, end_token: int = 0, workspace: Optional[torch.Tensor] = None,
+                   dev_status: Optional[torch.Tensor] = None):
+    """The num_select best continuations of each request's beams: scores_out
+    (float32), rows_out (the beam's row of logits) and tokens_out (int32), each
+    [num_requests, num_select], best first.  logits [num_rows, vocab] (float16 /
+    bfloat16 / float32; rows may be strided); scores float32 [num_rows];
+    cu_beams int32 [num_requests + 1]; allowed: bit masks, int32 [num_rows,
+    ceil(vocab / 32)]; ended: uint8 or bool [num_rows]."""
+    if not isinstance(logits, torch.Tensor) or not logits.is_cuda or logits.dim() != 2:
+        raise ValueError("logits must be a CUDA tensor [num_rows, vocab]")
+    if logits.dtype not in _LOGITS_CODE:
+        raise TypeError("unsupported dtype %s" % logits.dtype)
+    R, V = logits.shape
+    if V > 1 and logits.stride(1) != 1:
+        raise ValueError("the tokens of a row of logits must be contiguous")
+    stride = logits.stride(0) if R > 1 else V
+    _need(cu_beams, "cu_beams", torch.int32)
+    if cu_beams.dim() != 1 or cu_beams.shape[0] < 1:
+        raise ValueError("cu_beams must have num_requests + 1 entries")
+    B = cu_beams.shape[0] - 1
+    _need(scores_out, "scores_out", torch.float32)
+    if scores_out.dim() != 2:
+        raise ValueError("scores_out must be [num_requests, num_select]")
+    K = scores_out.shape[1]
+    _beside(cu_beams, "cu_beams", logits, torch.int32, (B + 1,))
+    _beside(scores, "scores", logits, torch.float32, (R,))
+    _beside(scores_out, "scores_out", logits, torch.float32, (B, K))
+    _beside(rows_out, "rows_out", logits, torch.int32, (B, K))
+    _beside(tokens_out, "tokens_out", logits, torch.int32, (B, K))
+    words = (V + 31) // 32
+    if allowed is not None:
+        _beside(allowed, "allowed", logits, torch.int32, (R, words))
+    if ended is not None:
+        _beside(ended, "ended", logits, torch.bool if ended.dtype == torch.bool else torch.uint8, (R,))
+    ws_bytes = 0
+    if workspace is not None:
+        _beside(workspace, "workspace", logits, workspace.dtype, workspace.shape)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _status_beside(dev_status, logits)
+    with torch.cuda.device(logits.device):
+        st = library().pa_beam_select(_ptr(scores_out), _ptr(rows_out), _ptr(tokens_out), _ptr(logits),
+                                      _LOGITS_CODE[logits.dtype], stride, V, R, _ptr(scores), _ptr(cu_beams), B,
+                                      _ptr(allowed), words, _ptr(ended), int(end_token), K, _ptr(workspace), ws_bytes,
+                                      _ptr(dev_status), _stream(logits))
+    _check(st, "pa_beam_select")
+
+
+class KVLayers:
+    """The layers' caches (KVCache, of one shape and type) that one block table
+    serves, as pa_beam_reorder takes them.  A program makes it once."""
+
+    def __init__(self, caches):
+        self.caches = list(caches)
+        if not self.caches:
+            raise ValueError("at least one layer's cache")
+        c = self.caches[0].k_cache
+        for x in self.caches:
+            if x.k_cache.shape != c.shape or x.k_cache.dtype != c.dtype or x.k_cache.device != c.device or \
+                    x.v_cache.device != c.device:
+                raise ValueError("the layers' caches must be alike and on one device")
+        self._array = (_Cache * len(self.caches))(*[x.c_struct() for x in self.caches])
+
+
+def pa_beam_reorder(layers: KVLayers, parents: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                    spare_blocks: torch.Tensor, block_table_out: torch.Tensor, seq_lens_out: torch.Tensor,
+                    slot_mapping_out: torch.Tensor, spare_used_out: torch.Tensor,
+                    dev_status: Optional[torch.Tensor] = None):
+    """Block tables, lengths and slots of the beams that go on: new row i from row
+    parents[i] (int32 [n], < 0: none) of block_table (int32 [rows, max_blocks]) and
+    seq_lens (int32 [rows]), each with one token more; partly filled blocks that
+    several rows would write into are copied to spare_blocks[i] (int32 [n]) in every
+    layer.  Out: tables int32 [n, max_blocks], lengths int32 [n], slots int64 [n],
+    which spares were used int32 [n]."""
+    if not isinstance(layers, KVLayers):
+        raise TypeError("layers must be KVLayers")
+    like = layers.caches[0].k_cache
+    _need(parents, "parents", torch.int32)
+    _need(block_table, "block_table", torch.int32)
+    if parents.dim() != 1 or block_table.dim() != 2:
+        raise ValueError("parents must be [n], block_table [rows, max_blocks]")
+    n, (rows, width) = parents.shape[0], block_table.shape
+    _beside(parents, "parents", like, torch.int32, (n,))
+    _beside(block_table, "block_table", like, torch.int32, (rows, width))
+    _beside(seq_lens, "seq_lens", like, torch.int32, (rows,))
+    _beside(spare_blocks, "spare_blocks", like, torch.int32, (n,))
+    _beside(block_table_out, "block_table_out", like, torch.int32, (n, width))
+    _beside(seq_lens_out, "seq_lens_out", like, torch.int32, (n,))
+    _beside(slot_mapping_out, "slot_mapping_out", like, torch.int64, (n,))
+    _beside(spare_used_out, "spare_used_out", like, torch.int32, (n,))
+    _status_beside(dev_status, like)
+    with torch.cuda.device(like.device):
+        st = library().pa_beam_reorder(layers._array, len(layers.caches), _ptr(parents), n, _ptr(block_table), rows,
+                                       width, _ptr(seq_lens), _ptr(spare_blocks), _ptr(block_table_out),
+                                       _ptr(seq_lens_out), _ptr(slot_mapping_out), _ptr(spare_used_out),
+                                       _ptr(dev_status), _stream(like))
+    _check(st, "pa_beam_reorder")
+
+
 def pa_slot_mapping(block_table, block_size: int, seq_idx, pos):
     """Host helper: slots of new tokens (numpy int32 table [B, max_blocks],
     seq_idx int32 [n], pos int64 [n]) -> numpy int64 [n]."""
@@ -666,6 +796,30 @@ class BlockPool:
         _check(library().pa_pool_release_window(self._h, seq_id, _clamp32(window), _clamp32(num_sinks), C.byref(n)),
                "pa_pool_release_window")
         return n.value
+
+    def reserve(self, n: int):
+        """The next n free blocks, the caller's own until reorder uses them or
+        unreserve gives them back."""
+        out = (C.c_int32 * max(n, 1))()
+        _check(library().pa_pool_reserve(self._h, n, out), "pa_pool_reserve")
+        return list(out[:n])
+
+    def unreserve(self, blocks):
+        n = len(blocks)
+        _check(library().pa_pool_unreserve(self._h, (C.c_int32 * max(n, 1))(*blocks), n), "pa_pool_unreserve")
+
+    def reorder(self, old_ids, new_ids, parents, spare_blocks):
+        """pa_beam_reorder's rule in the pool: the sequences new_ids, from
+        old_ids[parents[i]] each with a token more, take the place of old_ids.
+        Returns (slots, which spares were used)."""
+        n, m = len(new_ids), len(old_ids)
+        if len(parents) != n or len(spare_blocks) != n:
+            raise ValueError("parents and spare_blocks must have an entry for each new id")
+        slots, used = (C.c_int64 * max(n, 1))(), (C.c_int32 * max(n, 1))()
+        _check(library().pa_pool_reorder(self._h, (C.c_int64 * max(m, 1))(*old_ids), m,
+                                         (C.c_int64 * max(n, 1))(*new_ids), n, (C.c_int32 * max(n, 1))(*parents),
+                                         (C.c_int32 * max(n, 1))(*spare_blocks), slots, used), "pa_pool_reorder")
+        return list(slots[:n]), [bool(x) for x in used[:n]]
 
     def block_table(self, seq_ids, max_blocks: int):
         n = len(seq_ids)

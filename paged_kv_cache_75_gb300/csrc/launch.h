@@ -67,10 +67,10 @@ int blocks_per_sm(Kernel kern, int threads, int smem, LaunchCache& c) {
 // launch gap between back-to-back calls.  Every kernel launched this way calls
 // pdl_wait() before touching global memory.
 template <typename... Params, typename... Args>
-cudaError_t launch_pdl(void (*kern)(Params...), int grid, int block, int smem, cudaStream_t stream,
+cudaError_t launch_pdl(void (*kern)(Params...), dim3 grid, int block, int smem, cudaStream_t stream,
                        Args&&... args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(static_cast<unsigned>(block));
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = stream;

@@ -44,6 +44,7 @@ struct Pool {
     std::vector<int32_t> free_ring;       // the free list: `num_free` ids from `head` on, wrapping
     int64_t head = 0, num_free = 0;
     std::vector<int32_t> ref;
+    std::vector<char> reserved;  // held by the caller (pa_pool_reserve), of no sequence
     std::unordered_map<int64_t, Sequence> seqs;
 
     int32_t take() {
@@ -80,6 +81,7 @@ pa_status pa_pool_create(int64_t num_blocks, int32_t block_size, const int32_t* 
     std::vector<char> seen;
     try {
         p->ref.assign(static_cast<size_t>(num_blocks), 0);
+        p->reserved.assign(static_cast<size_t>(num_blocks), 0);
         p->free_ring.resize(static_cast<size_t>(num_blocks));
         if (free_order != nullptr) seen.assign(static_cast<size_t>(num_blocks), 0);
     } catch (const std::bad_alloc&) {
@@ -219,6 +221,106 @@ pa_status pa_pool_release_window(void* pool, int64_t seq_id, int32_t window, int
         s.released_to = joins && s.released_to > end ? s.released_to : end;
     }
     if (n_released_out) *n_released_out = n;
+    return PA_OK;
+}
+
+pa_status pa_pool_reserve(void* pool, int32_t n, int32_t* blocks_out) {
+    Pool* p = as_pool(pool);
+    if (p == nullptr || n < 0 || (n > 0 && blocks_out == nullptr)) return PA_ERR_INVALID_ARG;
+    if (n > p->num_free) return PA_ERR_OOM;
+    for (int32_t i = 0; i < n; ++i) {
+        blocks_out[i] = p->take();
+        p->reserved[blocks_out[i]] = 1;
+    }
+    return PA_OK;
+}
+
+pa_status pa_pool_unreserve(void* pool, const int32_t* blocks, int32_t n) {
+    Pool* p = as_pool(pool);
+    if (p == nullptr || n < 0 || (n > 0 && blocks == nullptr)) return PA_ERR_INVALID_ARG;
+    // every id a reserved block's, and once (2: met)
+    int32_t met = 0;
+    while (met < n && blocks[met] >= 0 && blocks[met] < p->num_blocks && p->reserved[blocks[met]] == 1)
+        p->reserved[blocks[met++]] = 2;
+    for (int32_t i = 0; i < met; ++i) p->reserved[blocks[i]] = 1;
+    if (met < n) return PA_ERR_INVALID_ARG;
+    for (int32_t i = 0; i < n; ++i) {
+        p->reserved[blocks[i]] = 0;
+        p->drop(blocks[i]);
+    }
+    return PA_OK;
+}
+
+// The host's half of pa_beam_reorder, by the same rule (row i and its parent's first
+// child), so both sides come to the same tables without exchanging them.  Everything is
+// checked and allocated before anything changes.
+pa_status pa_pool_reorder(void* pool, const int64_t* old_ids, int32_t num_old, const int64_t* new_ids, int32_t num_new,
+                          const int32_t* parents, const int32_t* spare_blocks, int64_t* slots_out,
+                          int32_t* spare_used_out) {
+    Pool* p = as_pool(pool);
+    if (p == nullptr || num_old < 0 || num_new < 0 || (num_old > 0 && old_ids == nullptr) ||
+        (num_new > 0 && (new_ids == nullptr || parents == nullptr || spare_blocks == nullptr)))
+        return PA_ERR_INVALID_ARG;
+    const int64_t bs = p->block_size;
+    std::vector<int64_t> added;  // new ids entered so far
+    try {
+        std::unordered_map<int64_t, int> old_at, new_at;
+        std::vector<Sequence*> old_seqs(static_cast<size_t>(num_old));
+        for (int32_t i = 0; i < num_old; ++i) {
+            auto it = p->seqs.find(old_ids[i]);
+            if (it == p->seqs.end() || !old_at.emplace(old_ids[i], i).second) return PA_ERR_INVALID_ARG;
+            old_seqs[i] = &it->second;
+        }
+        std::vector<Sequence> next(static_cast<size_t>(num_new));
+        std::vector<char> fresh(static_cast<size_t>(num_new), 0), kept(static_cast<size_t>(num_old), 0);
+        std::unordered_map<int32_t, int> spares;
+        for (int32_t i = 0; i < num_new; ++i) {
+            const bool known = p->seqs.count(new_ids[i]) != 0;
+            if (!new_at.emplace(new_ids[i], i).second || (known && !old_at.count(new_ids[i])) || parents[i] >= num_old)
+                return PA_ERR_INVALID_ARG;
+            if (parents[i] < 0) continue;
+            const Sequence& from = *old_seqs[parents[i]];
+            const int64_t rest = from.length % bs;
+            // a partly filled block that another sequence holds too is not the beam's
+            // to write into
+            if (from.length >= INT32_MAX || (rest != 0 && p->ref[from.blocks.back()] != 1)) return PA_ERR_INVALID_ARG;
+            fresh[i] = rest == 0 || kept[parents[i]];
+            kept[parents[i]] = 1;
+            if (fresh[i] && (spare_blocks[i] < 0 || spare_blocks[i] >= p->num_blocks ||
+                             p->reserved[spare_blocks[i]] != 1 || !spares.emplace(spare_blocks[i], i).second))
+                return PA_ERR_INVALID_ARG;
+            next[i].blocks.reserve(from.blocks.size() + (rest == 0));
+            next[i] = from;
+            if (rest == 0) next[i].blocks.push_back(spare_blocks[i]);
+            else if (fresh[i]) next[i].blocks.back() = spare_blocks[i];
+            ++next[i].length;
+        }
+        added.reserve(static_cast<size_t>(num_new));
+        for (int32_t i = 0; i < num_new; ++i)
+            if (p->seqs.emplace(new_ids[i], Sequence()).second) added.push_back(new_ids[i]);
+        // ---- nothing below fails ----
+        for (int32_t i = 0; i < num_new; ++i) {
+            const Sequence& s = next[i];
+            for (int32_t b : s.blocks)
+                if (b >= 0) p->ref[b] += 1;
+            if (fresh[i]) {
+                p->reserved[spare_blocks[i]] = 0;
+                p->ref[spare_blocks[i]] = 1;
+            }
+            if (slots_out != nullptr)
+                slots_out[i] = parents[i] < 0 ? -1 : static_cast<int64_t>(s.blocks.back()) * bs + (s.length - 1) % bs;
+            if (spare_used_out != nullptr) spare_used_out[i] = fresh[i];
+        }
+        for (int32_t i = 0; i < num_old; ++i) {
+            for (int32_t b : old_seqs[i]->blocks)
+                if (b >= 0) p->drop(b);
+            if (new_at.count(old_ids[i]) == 0) p->seqs.erase(old_ids[i]);
+        }
+        for (int32_t i = 0; i < num_new; ++i) p->seqs.find(new_ids[i])->second = std::move(next[i]);
+    } catch (const std::bad_alloc&) {
+        for (int64_t id : added) p->seqs.erase(id);
+        return PA_ERR_OOM;
+    }
     return PA_OK;
 }
 
