@@ -478,6 +478,48 @@ pa_status pa_decode_cascade(void* out, const void* q, pa_dtype q_dtype, const pa
                             void* workspace, size_t workspace_bytes, int32_t* dev_status, pa_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Varlen attention of groups of sequences that share a prefix, the prefix computed
+ * once for a group.  (pa_decode_cascade's sharing, "Как работает paged attention?
+ * (детально)" §3.3 and §7, for any number of query tokens a sequence: beams and
+ * samples that decode, short questions to one document, prompts behind a system
+ * prompt.)
+ *
+ * Computes what pa_prefill_varlen with causal != 0 computes (same arguments, same
+ * rounding, up to the order of sums).  Over a group's shared blocks its members' query
+ * rows stand together, 128 rows of one KV head's query heads to a tile, so the blocks
+ * are read and multiplied once per 128 / (num_heads / num_kv_heads) query tokens of the
+ * group instead of once per member; each member's own keys are attended apart, and a
+ * merge joins the parts by their log-sum-exp.
+ *
+ * cu_groups, shared_lens, num_groups, max_group_size, max_shared_len: as in
+ *   pa_decode_cascade.  Every query of a member comes after the shared tokens:
+ *   shared_lens[g] <= Lk - Lq of each member with queries.  A shared length that breaks
+ *   this or is no whole number of blocks, a member whose row differs over the
+ *   shared blocks, and bounds that do not hold are reported as PA_ERR_INVALID_ARG; the
+ *   group's rows are then unspecified.
+ * total_q: query rows of q and out; cu_seq_lens_q[num_seqs] <= total_q (otherwise
+ *   reported, and sequences past it are left out).  Rows behind the last sequence are
+ *   left as they are.
+ * workspace: pa_varlen_cascade_workspace_size(...) bytes with the same arguments,
+ *   16-byte aligned.
+ * scale > 0.  A value that some query of a sequence sees must be finite for the
+ *   sequence's other queries, and a shared one for the group's (pa_prefill_varlen's
+ *   rule); what other groups, and other members' own keys, hold takes no part.
+ * Supported: as pa_prefill_varlen (head_size 128, 16-bit caches); num_seqs + num_groups
+ *   <= 6144.
+ * ------------------------------------------------------------------------- */
+size_t pa_varlen_cascade_workspace_size(int32_t num_seqs, int64_t total_q, int32_t num_heads, int32_t num_kv_heads,
+                                        int32_t head_size, int32_t max_seqlen_q, int32_t max_seqlen_k,
+                                        int32_t max_shared_len, int32_t block_size);
+pa_status pa_varlen_cascade(void* out, const void* q, pa_dtype q_dtype, const pa_kv_cache* cache,
+                            const int32_t* block_table, int32_t max_blocks_per_seq, const int32_t* cu_seq_lens_q,
+                            const int32_t* cu_seq_lens_k, int32_t num_seqs, int64_t total_q, int32_t max_seqlen_q,
+                            int32_t max_seqlen_k, int32_t num_heads, float scale, const int32_t* cu_groups,
+                            const int32_t* shared_lens, int32_t num_groups, int32_t max_group_size,
+                            int32_t max_shared_len, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                            pa_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Beam search: selection.  ("Как работает paged attention? (детально)" 3.3 and the
  * vLLM paper summary name beam search among what shares blocks; its step is a selection,
  * then a reordering of the beams' states.)

@@ -97,6 +97,9 @@ def library():
                                                     sz, vp, vp], C.c_int),
             "pa_prefill_test_wait_timeout": ([vp, vp, C.c_int, pc, vp, i32, vp, vp, i32, i32, i32, i32, f32, i32, i32, vp,
                                               vp], C.c_int),
+            "pa_varlen_cascade_workspace_size": ([i32, i64, i32, i32, i32, i32, i32, i32, i32], sz),
+            "pa_varlen_cascade": ([vp, vp, C.c_int, pc, vp, i32, vp, vp, i32, i64, i32, i32, i32, f32, vp, vp, i32, i32,
+                                   i32, vp, sz, vp, vp], C.c_int),
             "pa_beam_select_workspace_size": ([i32, i32, i32], sz),
             "pa_beam_select": ([vp, vp, vp, vp, C.c_int, i64, i32, i32, vp, vp, i32, vp, i64, vp, i32, i32, vp, sz, vp,
                                 vp], C.c_int),
@@ -615,6 +618,49 @@ def pa_prefill_varlen_window(out: torch.Tensor, q: torch.Tensor, cache: KVCache,
     _check(_native().prefill_varlen_window(out, q, cache.k_cache, cache.v_cache, cache.k_scale, cache.v_scale,
                                            block_table, cu_seq_lens_q, cu_seq_lens_k, max_seqlen_q, max_seqlen_k, scale,
                                            window, num_sinks, dev_status), "pa_prefill_varlen_window")
+
+
+def pa_varlen_cascade_workspace_size(num_seqs, total_q, num_heads, num_kv_heads, head_size, max_seqlen_q, max_seqlen_k,
+                                     max_shared_len, block_size) -> int:
+    return int(library().pa_varlen_cascade_workspace_size(int(num_seqs), int(total_q), int(num_heads), int(num_kv_heads),
+                                                          int(head_size), int(max_seqlen_q), int(max_seqlen_k),
+                                                          int(max_shared_len), int(block_size)))
+
+
+def pa_varlen_cascade(out: torch.Tensor, q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
+                      cu_seq_lens_q: torch.Tensor, cu_seq_lens_k: torch.Tensor, max_seqlen_q: int, max_seqlen_k: int,
+                      scale: float, cu_groups: torch.Tensor, shared_lens: torch.Tensor, max_group_size: int,
+                      max_shared_len: int, workspace: torch.Tensor, dev_status: Optional[torch.Tensor] = None):
+    """pa_prefill_varlen (causal) for groups of sequences that share their first
+    blocks, one query token a sequence or several: cu_groups int32 [num_groups + 1]
+    (group g = sequences cu_groups[g] .. cu_groups[g+1]-1), shared_lens int32
+    [num_groups] (tokens, whole blocks, before every query of the group)."""
+    _need(q, "q")
+    if q.dim() != 3:
+        raise ValueError("q must be [total_q, num_heads, head_size]")
+    if cu_seq_lens_q.dim() != 1 or cu_seq_lens_q.shape[0] < 1 or shared_lens.dim() != 1 or block_table.dim() != 2:
+        raise ValueError("cu_seq_lens_q must have num_seqs + 1 entries, shared_lens one a group, block_table a row a sequence")
+    B, G = cu_seq_lens_q.shape[0] - 1, shared_lens.shape[0]
+    _beside(out, "out", q, q.dtype, q.shape)
+    _beside(cache.k_cache, "k_cache", q, cache.k_cache.dtype, cache.k_cache.shape)
+    if cache.head_size != q.shape[2]:
+        raise ValueError("the cache must have the queries' head size")
+    _beside(cu_seq_lens_q, "cu_seq_lens_q", q, torch.int32, (B + 1,))
+    _beside(cu_seq_lens_k, "cu_seq_lens_k", q, torch.int32, (B + 1,))
+    _beside(block_table, "block_table", q, torch.int32, (B, block_table.shape[1]))
+    _beside(cu_groups, "cu_groups", q, torch.int32, (G + 1,))
+    _beside(shared_lens, "shared_lens", q, torch.int32, (G,))
+    _beside(workspace, "workspace", q, workspace.dtype, workspace.shape)
+    _status_beside(dev_status, q)
+    cs = cache.c_struct()
+    with torch.cuda.device(q.device):
+        st = library().pa_varlen_cascade(_ptr(out), _ptr(q), torch_dtype_code(q.dtype), C.byref(cs), _ptr(block_table),
+                                         block_table.shape[1], _ptr(cu_seq_lens_q), _ptr(cu_seq_lens_k), B, q.shape[0],
+                                         int(max_seqlen_q), int(max_seqlen_k), q.shape[1], float(scale),
+                                         _ptr(cu_groups), _ptr(shared_lens), G, int(max_group_size),
+                                         int(max_shared_len), _ptr(workspace),
+                                         workspace.numel() * workspace.element_size(), _ptr(dev_status), _stream(q))
+    _check(st, "pa_varlen_cascade")
 
 
 _LOGITS_CODE = {torch.float16: PA_F16, torch.bfloat16: PA_BF16, torch.float32: PA_F32}
