@@ -530,8 +530,8 @@ pa_status pa_varlen_cascade(void* out, const void* q, pa_dtype q_dtype, const pa
  * The request's num_select largest, in descending order, ties to the lower row, then
  * the lower token: scores_out, rows_out (r, a row of logits), tokens_out (i), each device
  * [num_requests][num_select]; past the candidates there are -inf, -1, -1.  s is computed
- * beyond binary32 (its logarithm's sum to about 2^-27) and ordered so; scores_out is it rounded
- * once.
+ * to 48 bits (its logarithm's sum to about 2^-27) and ordered so; scores_out is it rounded
+ * once.  Scores below binary32's range are alike.
  *
  * logits: device, [num_rows][vocab] of dtype (F16, BF16 or F32), rows row_stride >=
  *   vocab elements apart, any alignment that the type has (16-byte aligned rows go
@@ -547,7 +547,7 @@ pa_status pa_varlen_cascade(void* out, const void* q, pa_dtype q_dtype, const pa
  * ended: device uint8 [num_rows], nullable: a row != 0 has one candidate, (r, end_token)
  *   with s = c_r; its logits are not read.
  * workspace: pa_beam_select_workspace_size(...) bytes, 16-byte aligned.
- * Supported: num_select <= 64.
+ * Supported: num_select <= 64, vocab <= 2^23.
  * ------------------------------------------------------------------------- */
 size_t pa_beam_select_workspace_size(int32_t num_rows, int32_t vocab, int32_t num_select);
 pa_status pa_beam_select(float* scores_out, int32_t* rows_out, int32_t* tokens_out, const void* logits,

@@ -9,7 +9,7 @@
 // order of x, so one pass over the logits gives both what the sum needs and the row's
 // K candidates.
 //
-// Rows kernel: a block holds a chunk of one row in registers, read once.  The K-th
+// Rows kernel: a block holds a chunk of one row in shared memory, read once.  The K-th
 // largest of its threads' maxima bounds the chunk's K-th largest element from below
 // (K threads hold an element of at least it), so what passes this threshold is a short
 // list that holds the chunk's K largest.  The threshold is found by bisection over
@@ -22,7 +22,7 @@
 // are left out of its sum and go into the row's in full, each exponential taken to about
 // 2^-30; the others' exponentials (ex2.approx, 2^-22 each, their errors unlike from
 // element to element) are summed 64 at a time in binary32 and from there on in units of
-// 2^-40, which no order of addition changes.  Logarithms and s are binary64.
+// 2^-40, which no order of addition changes.  s is the sum of two floats (48 bits).
 #include <cmath>
 
 #include "common.cuh"
@@ -33,14 +33,17 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxSelect = 64;
+constexpr int kRowsHere = 256;  // rows of a request whose sums stay in shared memory
+constexpr int kMaxVocab = 1 << 23;  // so many exponentials in units of 2^-40 fit 64 bits
 constexpr int kList = 1024;  // candidates a block ranks in shared memory
 constexpr float kLog2e = 1.4426950408889634f;
 
 // A row's log-sum-exp as its two terms: added up, a large maximum would take the
 // logarithm's bits with it.
 struct RowSum {
-    double top;      // the row's largest logit
-    double log_sum;  // log of the sum of exp(x - top); +inf: the row offers nothing
+    float top;           // the row's largest logit
+    float log_h, log_l;  // log of the sum of exp(x - top), as the sum of two floats; log_h = +inf: the row offers nothing
+    int32_t unused;
 };
 
 struct SelectParams {
@@ -95,6 +98,29 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return y;
 }
 
+// pairs of floats, one instruction for both
+__device__ __forceinline__ float2 f2_op(uint64_t r) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(r));
+    return f;
+}
+__device__ __forceinline__ uint64_t f2_of(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 f2_add(float2 a, float2 b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(f2_of(a.x, a.y)), "l"(f2_of(b.x, b.y)));
+    return f2_op(d);
+}
+__device__ __forceinline__ float2 f2_add(float2 a, float b) { return f2_add(a, make_float2(b, b)); }
+__device__ __forceinline__ float2 f2_mul(float2 a, float b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(f2_of(a.x, a.y)), "l"(f2_of(b, b)));
+    return f2_op(d);
+}
+
 // exp(a - b) in units of 2^-40, a <= b both finite, off by about 2^-30 of itself: the
 // difference as a sum of two floats, less a whole multiple n of ln 2 (three floats of
 // few bits, so that n times the first two is exact), then 1 + r + r^2/2 as a sum of two floats
@@ -134,16 +160,32 @@ __device__ __forceinline__ uint64_t exp_units(float a, float b) {
     return static_cast<uint64_t>(static_cast<int64_t>(__float2ll_rn(v * up)) + static_cast<int64_t>(__float2ll_rn(lo * up)));
 }
 
+// of two pairs of 16-bit floats, NaN where either is
 template <int DT>
-struct Logits {  // 16-bit types, two to a register
-    static constexpr int kVec = 8, kPerReg = 2;
-    __device__ static float2 get(uint32_t w) { return kv_pair<DT>(w); }
-    static constexpr uint32_t kNone = DT == PA_BF16 ? 0xff80u : 0xfc00u;  // -inf
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+    uint32_t d;
+    if constexpr (DT == PA_BF16) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+template <int DT, typename T>
+__device__ __forceinline__ float value_at(T x) {
+    if constexpr (DT == PA_F32) return __uint_as_float(x);
+    else return kv_pair<DT>(x).x;
+}
+
+template <int DT>
+struct Logits {  // 16-bit types, two to a word
+    using type = uint16_t;
+    static constexpr int kVec = 8, kPerWord = 2;
+    static constexpr type kNone = DT == PA_BF16 ? 0xff80u : 0xfc00u;  // -inf
 };
 template <>
 struct Logits<PA_F32> {
-    static constexpr int kVec = 4, kPerReg = 1;
-    static constexpr uint32_t kNone = 0xff800000u;
+    using type = uint32_t;
+    static constexpr int kVec = 4, kPerWord = 1;
+    static constexpr type kNone = 0xff800000u;
 };
 
 // sum over the block; all threads get it
@@ -160,13 +202,18 @@ __device__ __forceinline__ T block_sum(T v, T* scratch) {
     return v;
 }
 
-// The largest threshold found in a few steps that at least `want` of the block's keys
-// reach (fewer than want are above kNothing: the least that all of those reach).  Keys
-// that hold nothing are kNothing.  top: the block's largest key.  Stops early once no
-// more than 1.5 want reach it.
-__device__ __forceinline__ uint32_t threshold(uint32_t key, uint32_t top, int want) {
-    uint32_t lo = kNothing + 1, hi = top;  // count(lo) >= want once that is known; the answer is in [lo, hi]
-    if (__syncthreads_count(key > kNothing) <= want) return lo;
+// A threshold that at least `want` of the block's keys reach, found in a few steps: it
+// stops once no more than 1.5 want do, or at the largest such threshold.  Where no more
+// than `want` keys are above kNothing, what all of those reach.  top: the block's largest
+// key (> kNothing).  scratch: a word a warp.
+__device__ __forceinline__ uint32_t threshold(uint32_t key, uint32_t top, int want, uint32_t* scratch) {
+    if (__syncthreads_count(key > kNothing) <= want) return kNothing + 1;
+    // (the keys lie close together in the range of all floats: start from the least)
+    uint32_t lo = __reduce_min_sync(0xffffffffu, key > kNothing ? key : top), hi = top;
+    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = lo;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) lo = min(lo, scratch[w]);
     while (lo < hi) {
         const uint32_t mid = lo + (hi - lo + 1) / 2;
         const int n = __syncthreads_count(key >= mid);
@@ -180,25 +227,27 @@ __device__ __forceinline__ uint32_t threshold(uint32_t key, uint32_t top, int wa
     return lo;
 }
 
-// EPT elements a thread.  VEC: every row is 16-byte aligned and each thread reads
-// whole vectors; otherwise pairs of 16-bit elements (or single floats), with the rows'
-// own alignment.  Which element goes to which thread does not depend on a row's
+// EPT elements a thread, in groups of eight.  VEC: every row is 16-byte aligned and a group
+// is whole vectors of shared memory; otherwise it is four words' pairs of 16-bit elements
+// (eight floats), which lie in shared memory as they lie in memory, up to 14 bytes behind
+// a vector's start.  Which element goes to which thread does not depend on a row's
 // address, so equal rows get equal sums.
 template <int DT, int EPT, bool VEC>
 __global__ void __launch_bounds__(kThreads)
 beam_rows_kernel(const SelectParams p) {
     using L = Logits<DT>;
-    constexpr int kRegs = EPT / L::kPerReg;
-    constexpr int kGroupRegs = 8 / L::kPerReg;  // registers of eight elements
-    constexpr int kGroups = EPT / 8;
+    using T = typename L::type;
+    constexpr int kChunk = kThreads * EPT, kGroups = EPT / 8;
+    __shared__ __align__(16) T chunk_mem[kChunk + L::kVec];
     __shared__ uint64_t list[kList];
     __shared__ uint64_t scratch64[kThreads / 32];
     __shared__ float scratch[kThreads / 32];
+    __shared__ uint32_t scratch32[kThreads / 32];
     __shared__ int list_n;
 
     const int t = threadIdx.x;
     const int row = blockIdx.x / p.chunks_per_row, chunk = blockIdx.x - row * p.chunks_per_row;
-    const int first = chunk * (kThreads * EPT);
+    const int first = chunk * kChunk, here = min(kChunk, p.vocab - first);
     pdl_wait();
     pdl_trigger();
     uint8_t* base = p.chunks + static_cast<int64_t>(blockIdx.x) * p.chunk_bytes;
@@ -211,117 +260,106 @@ beam_rows_kernel(const SelectParams p) {
         if (t < p.select) keys[t] = 0;
         return;
     }
-    // ---- the chunk into registers ----
-    uint32_t raw[kRegs];
-    const uint32_t* bits = p.allowed == nullptr ? nullptr : p.allowed + row * p.allowed_stride;
-    // element of register i (its first)
-    auto index = [&](int i) -> int {
+    // ---- the chunk into shared memory, at its own offset from a vector's start ----
+    const T* src = static_cast<const T*>(p.logits) + row * p.row_stride + first;
+    const int skew = VEC ? 0 : static_cast<int>((reinterpret_cast<uintptr_t>(src) & 15u) / sizeof(T));
+    T* mem = chunk_mem + skew;  // element first + i is mem[i]
+    {
+        // whole vectors asynchronously, what is left at the two ends by element
+        const int lead = skew == 0 ? 0 : min(here, L::kVec - skew), vecs = (here - lead) / L::kVec;
+        for (int v = t; v < vecs; v += kThreads) {
+            const int at = lead + v * L::kVec;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(mem + at)),
+                         "l"(reinterpret_cast<uint64_t>(src + at))
+                         : "memory");
+        }
+        if (t < lead) mem[t] = src[t];
+        const int rest = lead + vecs * L::kVec;
+        if (rest + t < here) mem[rest + t] = src[rest + t];
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();
+    }
+    // element of group g that comes first, and how far the others are apart
+    auto place = [&](int g, int i) -> int {
         if constexpr (VEC) {
-            constexpr int kVecRegs = L::kVec / L::kPerReg;
-            return first + ((i / kVecRegs) * kThreads + t) * L::kVec + (i % kVecRegs) * L::kPerReg;
+            constexpr int kVecs = 8 / L::kVec;  // vectors of a group
+            return ((g * kVecs + i / L::kVec) * kThreads + t) * L::kVec + i % L::kVec;
         } else {
-            return first + (i * kThreads + t) * L::kPerReg;
+            constexpr int kWords = 8 / L::kPerWord;
+            return ((g * kWords + i / L::kPerWord) * kThreads + t) * L::kPerWord + i % L::kPerWord;
         }
     };
-    if constexpr (VEC) {
-        constexpr int kVecRegs = L::kVec / L::kPerReg;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            static_cast<const uint8_t*>(p.logits) + row * p.row_stride * (16 / L::kVec));
+    // what the row does not have or may not take: -inf
+    if (here < kChunk || p.allowed != nullptr) {
+        const uint32_t* bits = p.allowed == nullptr ? nullptr : p.allowed + row * p.allowed_stride;
+#pragma unroll 1
+        for (int g = 0; g < kGroups; ++g) {
 #pragma unroll
-        for (int j = 0; j < kRegs / kVecRegs; ++j) {
-            const int i0 = first + (j * kThreads + t) * L::kVec;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (i0 + L::kVec <= p.vocab) {
-                v = __ldcs(src + i0 / L::kVec);
-            } else if (i0 < p.vocab) {
-                // (the row's last, partly filled vector: past it the buffer may end)
-                if constexpr (L::kPerReg == 2) {
-                    const uint16_t* e = reinterpret_cast<const uint16_t*>(src) + i0;
-                    uint32_t w[4] = {0, 0, 0, 0};
+            for (int w = 0; w < 8; w += VEC ? L::kVec : L::kPerWord) {
+                // (these neighbours' bits lie in one word)
+                const int i0 = place(g, w);
+                uint32_t on = 0;
+                if (i0 < here) on = bits != nullptr ? __ldg(bits + ((first + i0) >> 5)) >> ((first + i0) & 31) : ~0u;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        if (i0 + k < p.vocab) w[k / 2] |= static_cast<uint32_t>(e[k]) << (16 * (k & 1));
-                    v = make_uint4(w[0], w[1], w[2], w[3]);
-                } else {
-                    const uint32_t* e = reinterpret_cast<const uint32_t*>(src) + i0;
-                    v.x = e[0];
-                    if (i0 + 1 < p.vocab) v.y = e[1];
-                    if (i0 + 2 < p.vocab) v.z = e[2];
-                }
+                for (int i = 0; i < (VEC ? L::kVec : L::kPerWord); ++i)
+                    if (i0 + i >= here || !(on >> i & 1u)) mem[i0 + i] = L::kNone;
             }
-            raw[j * kVecRegs] = v.x;
-            raw[j * kVecRegs + 1] = v.y;
-            raw[j * kVecRegs + 2] = v.z;
-            raw[j * kVecRegs + 3] = v.w;
         }
-    } else if constexpr (L::kPerReg == 2) {
-        const uint16_t* e = static_cast<const uint16_t*>(p.logits) + row * p.row_stride;
-        if ((reinterpret_cast<uintptr_t>(e) & 3u) == 0) {
+        if constexpr (!VEC) __syncthreads();  // (a pair's words hold other threads' elements too)
+    }
+    // group g's elements: two to a word (16-bit types), or one
+    constexpr int kGroupWords = 8 / L::kPerWord;
+    auto words = [&](int g, uint32_t (&w)[kGroupWords]) {
+        if constexpr (VEC) {
 #pragma unroll
-            for (int i = 0; i < kRegs; ++i) {
-                const int i0 = index(i);
-                raw[i] = 0;
-                if (i0 + 1 < p.vocab) raw[i] = __ldcs(reinterpret_cast<const uint32_t*>(e + i0));
-                else if (i0 < p.vocab) raw[i] = e[i0];
+            for (int v = 0; v < kGroupWords / 4; ++v) {
+                const uint4 x = *reinterpret_cast<const uint4*>(mem + place(g, v * L::kVec));
+                w[4 * v] = x.x;
+                w[4 * v + 1] = x.y;
+                w[4 * v + 2] = x.z;
+                w[4 * v + 3] = x.w;
+            }
+        } else if constexpr (L::kPerWord == 2) {
+            const uint32_t* m = reinterpret_cast<const uint32_t*>(chunk_mem + (skew & ~1));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int at = place(g, 2 * k) / 2;
+                w[k] = skew & 1 ? __funnelshift_r(m[at], m[at + 1], 16) : m[at];
             }
         } else {
-            // a pair lies in two words: (e - 1 + i0, e + i0), (e + i0 + 1, e + i0 + 2)
 #pragma unroll
-            for (int i = 0; i < kRegs; ++i) {
-                const int i0 = index(i);
-                raw[i] = 0;
-                if (i0 > 0 && i0 + 2 < p.vocab) {
-                    const uint32_t* w = reinterpret_cast<const uint32_t*>(e + i0 - 1);
-                    raw[i] = __funnelshift_r(__ldcs(w), __ldg(w + 1), 16);
-                } else if (i0 < p.vocab) {
-                    raw[i] = e[i0];
-                    if (i0 + 1 < p.vocab) raw[i] |= static_cast<uint32_t>(e[i0 + 1]) << 16;
-                }
-            }
+            for (int k = 0; k < 8; ++k) w[k] = mem[place(g, k)];
         }
-    } else {
-        const uint32_t* e = static_cast<const uint32_t*>(p.logits) + row * p.row_stride;
-#pragma unroll
-        for (int i = 0; i < kRegs; ++i) {
-            const int i0 = index(i);
-            raw[i] = i0 < p.vocab ? __ldcs(e + i0) : 0u;
-        }
-    }
-    // what the row does not have or may not take: -inf
-    const bool whole = first + kThreads * EPT <= p.vocab;
-    if (!whole || bits != nullptr) {
-#pragma unroll
-        for (int i = 0; i < kRegs; ++i) {
-            const int i0 = index(i);
-            // (the pair's two bits lie in one word: i0 is even)
-            uint32_t on = i0 < p.vocab ? ~0u : 0u;
-            if (bits != nullptr && i0 < p.vocab) on = __ldg(bits + (i0 >> 5)) >> (i0 & 31);
-            if constexpr (L::kPerReg == 2) {
-                if (i0 + 1 >= p.vocab) on &= 1u;
-                if (!(on & 1u)) raw[i] = (raw[i] & 0xffff0000u) | L::kNone;
-                if (!(on & 2u)) raw[i] = (raw[i] & 0xffffu) | (L::kNone << 16);
-            } else {
-                if (!(on & 1u)) raw[i] = L::kNone;
-            }
-        }
-    }
-    auto element = [&](int i) -> float {  // i-th of the thread's EPT
-        if constexpr (L::kPerReg == 2) {
-            const float2 f = L::get(raw[i / 2]);
+    };
+    auto element = [&](const uint32_t (&w)[kGroupWords], int i) -> float {
+        if constexpr (L::kPerWord == 2) {
+            const float2 f = kv_pair<DT>(w[i / 2]);
             return i & 1 ? f.y : f.x;
         } else {
-            return __uint_as_float(raw[i]);
+            return __uint_as_float(w[i]);
         }
     };
-    auto token = [&](int i) -> int { return index(i / L::kPerReg) + i % L::kPerReg; };
-    // ---- maxima: of every eight elements, the thread's, the block's ----
-    float gmax[kGroups], mine = -INFINITY;
+    auto largest = [&](const uint32_t (&w)[kGroupWords]) -> float {
+        if constexpr (L::kPerWord == 2) {
+            const float2 f = kv_pair<DT>(max2_nan<DT>(max2_nan<DT>(w[0], w[1]), max2_nan<DT>(w[2], w[3])));
+            return max_nan(f.x, f.y);
+        } else {
+            float m = __uint_as_float(w[0]);
 #pragma unroll
+            for (int i = 1; i < 8; ++i) m = max_nan(m, __uint_as_float(w[i]));
+            return m;
+        }
+    };
+    auto key_of = [&](int g, const uint32_t (&w)[kGroupWords], int i) -> uint64_t {
+        return (static_cast<uint64_t>(order_of(element(w, i))) << 32) | static_cast<uint32_t>(~(first + place(g, i)));
+    };
+    // ---- maxima: the thread's, the block's ----
+    float mine = -INFINITY;
+#pragma unroll 4
     for (int g = 0; g < kGroups; ++g) {
-        gmax[g] = element(8 * g);
-#pragma unroll
-        for (int i = 1; i < 8; ++i) gmax[g] = max_nan(gmax[g], element(8 * g + i));
-        mine = max_nan(mine, gmax[g]);
+        uint32_t w[kGroupWords];
+        words(g, w);
+        mine = max_nan(mine, largest(w));
     }
     float top = mine;
 #pragma unroll
@@ -337,36 +375,40 @@ beam_rows_kernel(const SelectParams p) {
         if (t < p.select) keys[t] = 0;
         return;
     }
-    const uint32_t cut = threshold(order_of(mine), order_of(top), p.select);
+    const uint32_t cut = threshold(order_of(mine), order_of(top), p.select, scratch32);
     const float cut_v = value_of(cut);
     // ---- the list of what reaches the threshold; the sum of the rest ----
     // exp(x - top): the difference first, which is exact or nearly so (a product with
     // log2 e first would lose what a large common part of the logits takes)
     auto exp_of = [&](float x) -> float { return exp2_approx((x - top) * kLog2e); };
-    float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
+    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 4
     for (int g = 0; g < kGroups; ++g) {
-        if (gmax[g] >= cut_v) {
-#pragma unroll
-            for (int i = 8 * g; i < 8 * g + 8; ++i) {
-                const float x = element(i);
+        uint32_t w[kGroupWords];
+        words(g, w);
+        if (largest(w) >= cut_v) {
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+                const float x = value_at<DT>(mem[place(g, i)]);
                 if (x >= cut_v) {
                     const int at = atomicAdd(&list_n, 1);
                     if (at < kList)
-                        list[at] = (static_cast<uint64_t>(order_of(x)) << 32) | static_cast<uint32_t>(~token(i));
+                        list[at] = (static_cast<uint64_t>(order_of(x)) << 32) | static_cast<uint32_t>(~(first + place(g, i)));
                 } else {
-                    sum0 += exp_of(x);
+                    sum.x += exp_of(x);
                 }
             }
         } else {
 #pragma unroll
-            for (int i = 8 * g; i < 8 * g + 8; i += 2) {
-                sum0 += exp_of(element(i));
-                sum1 += exp_of(element(i + 1));
+            for (int i = 0; i < 8; i += 2) {
+                float2 e = f2_mul(f2_add(make_float2(element(w, i), element(w, i + 1)), -top), kLog2e);
+                e.x = exp2_approx(e.x);
+                e.y = exp2_approx(e.y);
+                sum = f2_add(sum, e);
             }
         }
     }
-    uint64_t units = static_cast<uint64_t>(__float2ll_rn((sum0 + sum1) * 1099511627776.f));
+    uint64_t units = static_cast<uint64_t>(__float2ll_rn((sum.x + sum.y) * 1099511627776.f));
     __syncthreads();
     const int n = list_n;
     if (n <= kList) {
@@ -385,11 +427,15 @@ beam_rows_kernel(const SelectParams p) {
         uint64_t last = ~0ull;
         for (int r = 0; r < p.select; ++r) {
             uint64_t best = 0;
+#pragma unroll 1
+            for (int g = 0; g < kGroups; ++g) {
+                uint32_t w[kGroupWords];
+                words(g, w);
 #pragma unroll
-            for (int i = 0; i < EPT; ++i) {
-                const float x = element(i);
-                const uint64_t k = (static_cast<uint64_t>(order_of(x)) << 32) | static_cast<uint32_t>(~token(i));
-                if (x > -INFINITY && k < last && k > best) best = k;
+                for (int i = 0; i < 8; ++i) {
+                    const uint64_t k = key_of(g, w, i);
+                    if (element(w, i) > -INFINITY && k < last && k > best) best = k;
+                }
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) {
@@ -407,27 +453,46 @@ beam_rows_kernel(const SelectParams p) {
         }
         // the sum again, over all but the candidates
         units = 0;
+#pragma unroll 1
+        for (int g = 0; g < kGroups; ++g) {
+            uint32_t w[kGroupWords];
+            words(g, w);
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) {
-            const float x = element(i);
-            const uint64_t k = (static_cast<uint64_t>(order_of(x)) << 32) | static_cast<uint32_t>(~token(i));
-            if (x > -INFINITY && k < last)
-                units += static_cast<uint64_t>(__float2ll_rn(exp_of(x) * 1099511627776.f));
+            for (int i = 0; i < 8; ++i)
+                if (element(w, i) > -INFINITY && key_of(g, w, i) < last)
+                    units += static_cast<uint64_t>(__float2ll_rn(exp_of(element(w, i)) * 1099511627776.f));
         }
     }
     units = block_sum(units, scratch64);
     if (t == 0) *head = {units, top, 0};
 }
 
+// A number as the sum of two floats, hi the sum rounded: 48 bits.  Below binary32's range
+// it is hi alone.
+struct Two {
+    float hi, lo;
+};
+__device__ __forceinline__ Two two_sum(float a, float b) {
+    const float s = a + b, bb = s - a;
+    return {s, s > -INFINITY ? (a - (s - bb)) + (b - bb) : 0.f};
+}
+__device__ __forceinline__ Two two_add(Two a, Two b) {
+    Two s = two_sum(a.hi, b.hi);
+    if (!(s.hi > -INFINITY)) return s;
+    s.lo += a.lo + b.lo;
+    return two_sum(s.hi, s.lo);
+}
+
 struct Candidate {
-    double s;
+    Two s;
     uint64_t key;  // the logit's order, then the token's complement
     int32_t row;
 };
 // c stands before d: by score, then row; of one row by logit (a large maximum can take
 // the difference from their scores), then token
 __device__ __forceinline__ bool before(const Candidate& c, const Candidate& d) {
-    if (c.s != d.s) return c.s > d.s;
+    if (c.s.hi != d.s.hi) return c.s.hi > d.s.hi;
+    if (c.s.lo != d.s.lo) return c.s.lo > d.s.lo;
     if (c.row != d.row) return c.row < d.row;
     return c.key > d.key;
 }
@@ -437,6 +502,7 @@ __global__ void __launch_bounds__(kThreads)
 beam_requests_kernel(const SelectParams p) {
     __shared__ Candidate list[kList];
     __shared__ Candidate warp_best[kThreads / 32];
+    __shared__ RowSum row_sums[kRowsHere];
     __shared__ uint32_t scratch[kThreads / 32];
     __shared__ int list_n;
     pdl_wait();
@@ -453,7 +519,8 @@ beam_requests_kernel(const SelectParams p) {
         return p.chunks + (static_cast<int64_t>(row) * S + c) * p.chunk_bytes;
     };
     if (t == 0) list_n = 0;
-    // ---- each row's log-sum-exp: a warp takes a row ----
+    // ---- each row's log-sum-exp: a warp takes a row, then a thread its logarithm ----
+    RowSum* sums = r1 - r0 <= kRowsHere ? row_sums : p.sums + r0;
     for (int row = r0 + warp; row < r1; row += kThreads / 32) {
         const float score = p.scores[row];
         if (!(score < INFINITY) && lane == 0) report(p.status, PA_ERR_INVALID_ARG);
@@ -467,31 +534,37 @@ beam_requests_kernel(const SelectParams p) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         bad = __any_sync(0xffffffffu, bad);
-        double log_sum = INFINITY;
-        if (bad) {
-            if (lane == 0) report(p.status, PA_ERR_INVALID_ARG);
-        } else if (top > -INFINITY) {
-            uint64_t units = 0;
+        if (bad && lane == 0) report(p.status, PA_ERR_INVALID_ARG);
+        uint64_t units = 0;
+        if (!bad && top > -INFINITY) {
             for (int i = lane; i < S * K; i += 32) {
                 const int c = i / K;
                 const uint64_t k = reinterpret_cast<const uint64_t*>(head_of(row, c) + sizeof(ChunkHead))[i - c * K];
                 if (k != 0) units += exp_units(value_of(static_cast<uint32_t>(k >> 32)), top);
             }
             // (a chunk's units count against its own maximum)
-            double rest = 0.0;
             for (int c = lane; c < S; c += 32) {
                 const ChunkHead h = *reinterpret_cast<const ChunkHead*>(head_of(row, c));
-                if (h.sum != 0)
-                    rest += static_cast<double>(h.sum) * (static_cast<double>(exp_units(h.top, top)) * kUnit);
+                const uint64_t e = h.sum != 0 ? exp_units(h.top, top) : 0;
+                units += (__umul64hi(h.sum, e) << 24) | (h.sum * e >> 40);
             }
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                units += __shfl_xor_sync(0xffffffffu, units, o);
-                rest += __shfl_xor_sync(0xffffffffu, rest, o);
-            }
-            log_sum = log((static_cast<double>(units) + rest) * kUnit);
+            for (int o = 16; o > 0; o >>= 1) units += __shfl_xor_sync(0xffffffffu, units, o);
         }
-        if (lane == 0) p.sums[row] = {top, log_sum};
+        if (lane == 0) {
+            // (the units wait where the logarithm goes)
+            sums[row - r0].top = top;
+            sums[row - r0].log_h = __uint_as_float(static_cast<uint32_t>(units));
+            sums[row - r0].log_l = __uint_as_float(static_cast<uint32_t>(units >> 32));
+        }
+    }
+    __syncthreads();
+    for (int r = t; r < r1 - r0; r += kThreads) {
+        const uint64_t units =
+            __float_as_uint(sums[r].log_h) | static_cast<uint64_t>(__float_as_uint(sums[r].log_l)) << 32;
+        const double l = units != 0 ? log(static_cast<double>(units) * kUnit) : 0.0;
+        sums[r].log_h = units != 0 ? static_cast<float>(l) : INFINITY;
+        sums[r].log_l = static_cast<float>(l - static_cast<float>(l));
     }
     __syncthreads();
     // ---- candidates: slot i of the request's (row, chunk, rank); an ended row has one ----
@@ -502,20 +575,21 @@ beam_requests_kernel(const SelectParams p) {
         const float score = p.scores[c.row];
         if (!(score > -INFINITY && score < INFINITY)) return false;
         if (p.ended != nullptr && p.ended[c.row] != 0) {
-            c.s = score;
+            c.s = {score, 0.f};
             c.key = static_cast<uint32_t>(~p.end_token);
             return j == 0;
         }
         const int chunk = j / K;
         c.key = reinterpret_cast<const uint64_t*>(head_of(c.row, chunk) + sizeof(ChunkHead))[j - chunk * K];
-        const RowSum sum = p.sums[c.row];
-        if (c.key == 0 || sum.log_sum == INFINITY) return false;
-        const double x = value_of(static_cast<uint32_t>(c.key >> 32));
-        c.s = static_cast<double>(score) + ((x - sum.top) - sum.log_sum);
+        const RowSum sum = sums[c.row - r0];
+        if (c.key == 0 || sum.log_h == INFINITY) return false;
+        // score + ((x - top) - log)
+        const float x = value_of(static_cast<uint32_t>(c.key >> 32));
+        c.s = two_add(two_add(two_sum(x, -sum.top), {-sum.log_h, -sum.log_l}), {score, 0.f});
         return true;
     };
-    // (a score's float keeps the scores' order, so it serves as the threshold's key)
-    auto key_of = [](double s) -> uint32_t { return order_of(fmaxf(static_cast<float>(s), -3.4028234e38f)); };
+    // (the score's float keeps the scores' order, so it serves as the threshold's key)
+    auto key_of = [](Two s) -> uint32_t { return order_of(fmaxf(s.hi, -3.4028234e38f)); };
     uint32_t mine = kNothing;
     for (int64_t i = t; i < total; i += kThreads) {
         Candidate c;
@@ -526,7 +600,7 @@ beam_requests_kernel(const SelectParams p) {
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) top = max(top, scratch[w]);
-    const uint32_t cut = top == kNothing ? kNothing + 1 : threshold(mine, top, K);
+    const uint32_t cut = top == kNothing ? kNothing + 1 : threshold(mine, top, K, scratch);
     if (mine >= cut) {
         for (int64_t i = t; i < total; i += kThreads) {
             Candidate c;
@@ -539,11 +613,11 @@ beam_requests_kernel(const SelectParams p) {
     __syncthreads();
     const int n = list_n;
     auto put = [&](int rank, const Candidate& c) {
-        p.scores_out[out0 + rank] = static_cast<float>(c.s);
+        p.scores_out[out0 + rank] = c.s.hi;
         p.rows_out[out0 + rank] = c.row;
         p.tokens_out[out0 + rank] = c.row < 0 ? -1 : static_cast<int32_t>(~static_cast<uint32_t>(c.key));
     };
-    const Candidate none{-INFINITY, 0, -1};
+    const Candidate none{{-INFINITY, 0.f}, 0, -1};
     if (n <= kList) {
         for (int i = t; i < n; i += kThreads) {
             const Candidate c = list[i];
@@ -555,7 +629,7 @@ beam_requests_kernel(const SelectParams p) {
         return;
     }
     // more than the list holds: one a round, the first behind the last one
-    Candidate last{INFINITY, 0, -1};
+    Candidate last{{INFINITY, 0.f}, 0, -1};
     for (int r = 0; r < K; ++r) {
         Candidate best = none;
         for (int64_t i = t; i < total; i += kThreads) {
@@ -567,8 +641,8 @@ beam_requests_kernel(const SelectParams p) {
         };
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
-            const Candidate c{__shfl_xor_sync(0xffffffffu, best.s, o), __shfl_xor_sync(0xffffffffu, best.key, o),
-                              __shfl_xor_sync(0xffffffffu, best.row, o)};
+            const Candidate c{{__shfl_xor_sync(0xffffffffu, best.s.hi, o), __shfl_xor_sync(0xffffffffu, best.s.lo, o)},
+                              __shfl_xor_sync(0xffffffffu, best.key, o), __shfl_xor_sync(0xffffffffu, best.row, o)};
             join(c);
         }
         __syncthreads();
@@ -622,7 +696,7 @@ extern "C" pa_status pa_beam_select(float* scores_out, int32_t* rows_out, int32_
                                     int32_t* dev_status, pa_stream_t stream) {
     if (dtype != PA_F16 && dtype != PA_BF16 && dtype != PA_F32) return PA_ERR_UNSUPPORTED;
     if (num_requests < 0 || num_rows < 0 || vocab <= 0 || num_select <= 0 || row_stride < vocab) return PA_ERR_INVALID_ARG;
-    if (num_select > kMaxSelect) return PA_ERR_UNSUPPORTED;
+    if (num_select > kMaxSelect || vocab > kMaxVocab) return PA_ERR_UNSUPPORTED;
     if (num_requests == 0) return PA_OK;
     if (scores_out == nullptr || rows_out == nullptr || tokens_out == nullptr || cu_beams == nullptr)
         return PA_ERR_INVALID_ARG;

@@ -26,7 +26,7 @@ def select(lib, **kw):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(dtype=pk.PA_FP8_E4M3), 2), (dict(dtype=9), 2), (dict(k=65), 2), (dict(k=0), 1), (dict(vocab=0), 1),
+    (dict(dtype=pk.PA_FP8_E4M3), 2), (dict(dtype=9), 2), (dict(k=65), 2), (dict(vocab=(1 << 23) + 1, stride=1 << 24), 2), (dict(k=0), 1), (dict(vocab=0), 1),
     (dict(stride=999), 1), (dict(rows=-1), 1), (dict(requests=-1), 1), (dict(logits=None), 1), (dict(scores=None), 1),
     (dict(cu=None), 1), (dict(scores_out=None), 1), (dict(rows_out=None), 1), (dict(tokens_out=None), 1),
     (dict(logits=FAKE + 1), 1), (dict(logits=FAKE + 2, dtype=pk.PA_F32), 1), (dict(allowed=FAKE, allowed_stride=31), 1),
