@@ -162,6 +162,8 @@ def _native():
                 torch._C._cuda_getDevice, torch._C._cuda_setDevice, torch._C._cuda_getCurrentRawStream,
                 *[C.cast(f, C.c_void_p).value for f in (L.pa_qk_norm_rope, L.pa_qk_norm_rope_write, L.pa_decode_window,
                                                         L.pa_prefill_varlen_window)])
+        m.setup_beams(torch.uint8, torch.bool, *[C.cast(f, C.c_void_p).value for f in (
+            L.pa_varlen_cascade, L.pa_beam_select, L.pa_beam_reorder)])
         _native_mod = m
     return _native_mod
 
@@ -635,51 +637,9 @@ def pa_varlen_cascade(out: torch.Tensor, q: torch.Tensor, cache: KVCache, block_
     blocks, one query token a sequence or several: cu_groups int32 [num_groups + 1]
     (group g = sequences cu_groups[g] .. cu_groups[g+1]-1), shared_lens int32
     [num_groups] (tokens, whole blocks, before every query of the group)."""
-    _need(q, "q")
-    if q.dim() != 3:
-        raise ValueError("q must be [total_q, num_heads, head_size]")
-    if cu_seq_lens_q.dim() != 1 or cu_seq_lens_q.shape[0] < 1 or shared_lens.dim() != 1 or block_table.dim() != 2:
-        raise ValueError("cu_seq_lens_q must have num_seqs + 1 entries, shared_lens one a group, block_table a row a sequence")
-    B, G = cu_seq_lens_q.shape[0] - 1, shared_lens.shape[0]
-    _beside(out, "out", q, q.dtype, q.shape)
-    _beside(cache.k_cache, "k_cache", q, cache.k_cache.dtype, cache.k_cache.shape)
-    if cache.head_size != q.shape[2]:
-        raise ValueError("the cache must have the queries' head size")
-    _beside(cu_seq_lens_q, "cu_seq_lens_q", q, torch.int32, (B + 1,))
-    _beside(cu_seq_lens_k, "cu_seq_lens_k", q, torch.int32, (B + 1,))
-    _beside(block_table, "block_table", q, torch.int32, (B, block_table.shape[1]))
-    _beside(cu_groups, "cu_groups", q, torch.int32, (G + 1,))
-    _beside(shared_lens, "shared_lens", q, torch.int32, (G,))
-    _beside(workspace, "workspace", q, workspace.dtype, workspace.shape)
-    _status_beside(dev_status, q)
-    cs = cache.c_struct()
-    with torch.cuda.device(q.device):
-        st = library().pa_varlen_cascade(_ptr(out), _ptr(q), torch_dtype_code(q.dtype), C.byref(cs), _ptr(block_table),
-                                         block_table.shape[1], _ptr(cu_seq_lens_q), _ptr(cu_seq_lens_k), B, q.shape[0],
-                                         int(max_seqlen_q), int(max_seqlen_k), q.shape[1], float(scale),
-                                         _ptr(cu_groups), _ptr(shared_lens), G, int(max_group_size),
-                                         int(max_shared_len), _ptr(workspace),
-                                         workspace.numel() * workspace.element_size(), _ptr(dev_status), _stream(q))
-    _check(st, "pa_varlen_cascade")
-
-
-_LOGITS_CODE = {torch.float16: PA_F16, torch.bfloat16: PA_BF16, torch.float32: PA_F32}
-
-
-def _beside(t, name, like, dtype, shape):
-    """A contiguous CUDA tensor of that type and shape on `like`'s device."""
-    _need(t, name, dtype)
-    if t.device != like.device:
-        raise ValueError("%s must be on %s" % (name, like.device))
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError("%s must be %s" % (name, list(shape)))
-
-
-def _status_beside(t, like):
-    if t is not None:
-        _beside(t, "dev_status", like, torch.int32, t.shape)
-        if t.numel() < 1:
-            raise ValueError("dev_status must have an entry")
+    _check(_native().varlen_cascade(out, q, cache.k_cache, cache.v_cache, cache.k_scale, cache.v_scale, block_table,
+                                    cu_seq_lens_q, cu_seq_lens_k, max_seqlen_q, max_seqlen_k, scale, cu_groups, shared_lens,
+                                    max_group_size, max_shared_len, workspace, dev_status), "pa_varlen_cascade")
 
 
 def pa_beam_select_workspace_size(num_rows, vocab, num_select) -> int:
@@ -696,43 +656,8 @@ def pa_beam_select(scores_out: torch.Tensor, rows_out: torch.Tensor, tokens_out:
     bfloat16 / float32; rows may be strided); scores float32 [num_rows];
     cu_beams int32 [num_requests + 1]; allowed: bit masks, int32 [num_rows,
     ceil(vocab / 32)]; ended: uint8 or bool [num_rows]."""
-    if not isinstance(logits, torch.Tensor) or not logits.is_cuda or logits.dim() != 2:
-        raise ValueError("logits must be a CUDA tensor [num_rows, vocab]")
-    if logits.dtype not in _LOGITS_CODE:
-        raise TypeError("unsupported dtype %s" % logits.dtype)
-    R, V = logits.shape
-    if V > 1 and logits.stride(1) != 1:
-        raise ValueError("the tokens of a row of logits must be contiguous")
-    stride = logits.stride(0) if R > 1 else V
-    _need(cu_beams, "cu_beams", torch.int32)
-    if cu_beams.dim() != 1 or cu_beams.shape[0] < 1:
-        raise ValueError("cu_beams must have num_requests + 1 entries")
-    B = cu_beams.shape[0] - 1
-    _need(scores_out, "scores_out", torch.float32)
-    if scores_out.dim() != 2:
-        raise ValueError("scores_out must be [num_requests, num_select]")
-    K = scores_out.shape[1]
-    _beside(cu_beams, "cu_beams", logits, torch.int32, (B + 1,))
-    _beside(scores, "scores", logits, torch.float32, (R,))
-    _beside(scores_out, "scores_out", logits, torch.float32, (B, K))
-    _beside(rows_out, "rows_out", logits, torch.int32, (B, K))
-    _beside(tokens_out, "tokens_out", logits, torch.int32, (B, K))
-    words = (V + 31) // 32
-    if allowed is not None:
-        _beside(allowed, "allowed", logits, torch.int32, (R, words))
-    if ended is not None:
-        _beside(ended, "ended", logits, torch.bool if ended.dtype == torch.bool else torch.uint8, (R,))
-    ws_bytes = 0
-    if workspace is not None:
-        _beside(workspace, "workspace", logits, workspace.dtype, workspace.shape)
-        ws_bytes = workspace.numel() * workspace.element_size()
-    _status_beside(dev_status, logits)
-    with torch.cuda.device(logits.device):
-        st = library().pa_beam_select(_ptr(scores_out), _ptr(rows_out), _ptr(tokens_out), _ptr(logits),
-                                      _LOGITS_CODE[logits.dtype], stride, V, R, _ptr(scores), _ptr(cu_beams), B,
-                                      _ptr(allowed), words, _ptr(ended), int(end_token), K, _ptr(workspace), ws_bytes,
-                                      _ptr(dev_status), _stream(logits))
-    _check(st, "pa_beam_select")
+    _check(_native().beam_select(scores_out, rows_out, tokens_out, logits, scores, cu_beams, allowed, ended, end_token,
+                                 workspace, dev_status), "pa_beam_select")
 
 
 class KVLayers:
@@ -749,6 +674,8 @@ class KVLayers:
                     x.v_cache.device != c.device:
                 raise ValueError("the layers' caches must be alike and on one device")
         self._array = (_Cache * len(self.caches))(*[x.c_struct() for x in self.caches])
+        # what the native call reads
+        self._args = (C.addressof(self._array), len(self.caches), c)
 
 
 def pa_beam_reorder(layers: KVLayers, parents: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
@@ -763,27 +690,8 @@ def pa_beam_reorder(layers: KVLayers, parents: torch.Tensor, block_table: torch.
     which spares were used int32 [n]."""
     if not isinstance(layers, KVLayers):
         raise TypeError("layers must be KVLayers")
-    like = layers.caches[0].k_cache
-    _need(parents, "parents", torch.int32)
-    _need(block_table, "block_table", torch.int32)
-    if parents.dim() != 1 or block_table.dim() != 2:
-        raise ValueError("parents must be [n], block_table [rows, max_blocks]")
-    n, (rows, width) = parents.shape[0], block_table.shape
-    _beside(parents, "parents", like, torch.int32, (n,))
-    _beside(block_table, "block_table", like, torch.int32, (rows, width))
-    _beside(seq_lens, "seq_lens", like, torch.int32, (rows,))
-    _beside(spare_blocks, "spare_blocks", like, torch.int32, (n,))
-    _beside(block_table_out, "block_table_out", like, torch.int32, (n, width))
-    _beside(seq_lens_out, "seq_lens_out", like, torch.int32, (n,))
-    _beside(slot_mapping_out, "slot_mapping_out", like, torch.int64, (n,))
-    _beside(spare_used_out, "spare_used_out", like, torch.int32, (n,))
-    _status_beside(dev_status, like)
-    with torch.cuda.device(like.device):
-        st = library().pa_beam_reorder(layers._array, len(layers.caches), _ptr(parents), n, _ptr(block_table), rows,
-                                       width, _ptr(seq_lens), _ptr(spare_blocks), _ptr(block_table_out),
-                                       _ptr(seq_lens_out), _ptr(slot_mapping_out), _ptr(spare_used_out),
-                                       _ptr(dev_status), _stream(like))
-    _check(st, "pa_beam_reorder")
+    _check(_native().beam_reorder(*layers._args, parents, block_table, seq_lens, spare_blocks, block_table_out, seq_lens_out,
+                                  slot_mapping_out, spare_used_out, dev_status), "pa_beam_reorder")
 
 
 def pa_slot_mapping(block_table, block_size: int, seq_idx, pos):

@@ -46,6 +46,12 @@ struct RowSum {
     int32_t unused;
 };
 
+struct ChunkHead {
+    uint64_t sum;  // of exp(x - top) over what is not in the chunk's list, in units of 2^-40
+    float top;     // -inf: the chunk offers nothing
+    int32_t bad;   // an allowed logit is NaN or +inf
+};
+
 struct SelectParams {
     float* scores_out;
     int32_t* rows_out;
@@ -56,8 +62,9 @@ struct SelectParams {
     const uint32_t* allowed;  // NULL: every token
     const uint8_t* ended;     // NULL: no row
     int32_t* status;
-    uint8_t* chunks;  // [num_rows][chunks_per_row] of chunk_bytes: header, then `select` keys
-    RowSum* sums;  // [num_rows]
+    RowSum* sums;              // [num_rows]
+    ChunkHead* heads;   // [num_rows][chunks_per_row]
+    uint64_t* keys;            // [num_rows][chunks_per_row][select]
     int64_t row_stride;
     int64_t allowed_stride;
     int32_t vocab;
@@ -66,16 +73,8 @@ struct SelectParams {
     int32_t select;
     int32_t end_token;
     int32_t chunks_per_row;
-    int32_t chunk_bytes;
 };
 
-struct ChunkHead {
-    uint64_t sum;  // of exp(x - top) over what is not in the chunk's list, in units of 2^-40
-    float top;     // -inf: the chunk offers nothing
-    int32_t bad;   // an allowed logit is NaN or +inf
-};
-static_assert(sizeof(ChunkHead) == 16, "the keys follow at 16 bytes");
-constexpr double kUnit = 1.0 / (1ull << 40);
 
 // Order-preserving integer of a float (+0 and -0 alike).
 __device__ __forceinline__ uint32_t order_of(float x) {
@@ -98,28 +97,11 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return y;
 }
 
-// pairs of floats, one instruction for both
-__device__ __forceinline__ float2 f2_op(uint64_t r) {
-    float2 f;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(r));
-    return f;
-}
-__device__ __forceinline__ uint64_t f2_of(float x, float y) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ float2 f2_add(float2 a, float2 b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(f2_of(a.x, a.y)), "l"(f2_of(b.x, b.y)));
-    return f2_op(d);
-}
-__device__ __forceinline__ float2 f2_add(float2 a, float b) { return f2_add(a, make_float2(b, b)); }
-__device__ __forceinline__ float2 f2_mul(float2 a, float b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(f2_of(a.x, a.y)), "l"(f2_of(b, b)));
-    return f2_op(d);
-}
+// ln 2 as 12 bits, 12 bits and the rest
+constexpr double kLn2 = 0.693147180559945309417;
+constexpr float kLn2a = static_cast<float>(static_cast<int>(kLn2 * 4096.0)) / 4096.f;
+constexpr float kLn2b = static_cast<float>(static_cast<int>((kLn2 - kLn2a) * 16777216.0)) / 16777216.f;
+constexpr float kLn2c = static_cast<float>(kLn2 - kLn2a - kLn2b);
 
 // exp(a - b) in units of 2^-40, a <= b both finite, off by about 2^-30 of itself: the
 // difference as a sum of two floats, less a whole multiple n of ln 2 (three floats of
@@ -131,16 +113,11 @@ __device__ __forceinline__ uint64_t exp_units(float a, float b) {
     const float back = d - a;
     const float dl = (a - (d - back)) - (b + back);  // d + dl = a - b exactly
     const float n = rintf(d * kLog2e);
-    // ln 2 = c0 + c1 + c2: 12 bits, 12 bits, the rest
-    constexpr double kLn2 = 0.693147180559945309417;
-    constexpr float c0 = static_cast<float>(static_cast<int>(kLn2 * 4096.0)) / 4096.f;
-    constexpr float c1 = static_cast<float>(static_cast<int>((kLn2 - c0) * 16777216.0)) / 16777216.f;
-    constexpr float c2 = static_cast<float>(kLn2 - c0 - c1);
-    const float h = fmaf(-n, c0, d);  // exact: d and n c0 nearly cancel
-    const float t = -n * c1;          // exact
+    const float h = fmaf(-n, kLn2a, d);  // exact: d and n kLn2a nearly cancel
+    const float t = -n * kLn2b;          // exact
     const float rh = h + t;
     const float bb = rh - h;
-    const float rl = ((h - (rh - bb)) + (t - bb)) + fmaf(-n, c2, dl);
+    const float rl = ((h - (rh - bb)) + (t - bb)) + fmaf(-n, kLn2c, dl);
     const float r = rh + rl;
     // r^3/6 + r^4/24 + ..., |r| <= 0.35
     float q = 1.f / 40320.f;
@@ -205,18 +182,20 @@ __device__ __forceinline__ T block_sum(T v, T* scratch) {
 // A threshold that at least `want` of the block's keys reach, found in a few steps: it
 // stops once no more than 1.5 want do, or at the largest such threshold.  Where no more
 // than `want` keys are above kNothing, what all of those reach.  top: the block's largest
-// key (> kNothing).  scratch: a word a warp.
+// key (> kNothing).  DROP: low bits that say nothing (a 16-bit type's values: a step a
+// value, not 2^16 of them).  scratch: a word a warp.
+template <int DROP>
 __device__ __forceinline__ uint32_t threshold(uint32_t key, uint32_t top, int want, uint32_t* scratch) {
     if (__syncthreads_count(key > kNothing) <= want) return kNothing + 1;
     // (the keys lie close together in the range of all floats: start from the least)
-    uint32_t lo = __reduce_min_sync(0xffffffffu, key > kNothing ? key : top), hi = top;
+    uint32_t lo = __reduce_min_sync(0xffffffffu, key > kNothing ? key : top) >> DROP, hi = top >> DROP;
     if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = lo;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) lo = min(lo, scratch[w]);
     while (lo < hi) {
         const uint32_t mid = lo + (hi - lo + 1) / 2;
-        const int n = __syncthreads_count(key >= mid);
+        const int n = __syncthreads_count(key >> DROP >= mid);
         if (n >= want) {
             lo = mid;
             if (n <= want + want / 2) break;
@@ -224,63 +203,20 @@ __device__ __forceinline__ uint32_t threshold(uint32_t key, uint32_t top, int wa
             hi = mid - 1;
         }
     }
-    return lo;
+    return lo << DROP;
 }
 
-// EPT elements a thread, in groups of eight.  VEC: every row is 16-byte aligned and a group
-// is whole vectors of shared memory; otherwise it is four words' pairs of 16-bit elements
-// (eight floats), which lie in shared memory as they lie in memory, up to 14 bytes behind
-// a vector's start.  Which element goes to which thread does not depend on a row's
-// address, so equal rows get equal sums.
+// One chunk's list and sum (see beam_rows_kernel): element first + i is mem[i].
 template <int DT, int EPT, bool VEC>
-__global__ void __launch_bounds__(kThreads)
-beam_rows_kernel(const SelectParams p) {
+__device__ __forceinline__ void rows_chunk(const SelectParams& p, typename Logits<DT>::type* mem,
+                                           const typename Logits<DT>::type* chunk_mem, int skew, int first, int here,
+                                           int64_t row, ChunkHead* head, uint64_t* keys, uint64_t* list, int& list_n,
+                                           uint64_t* scratch64, float* scratch, uint32_t* scratch32) {
     using L = Logits<DT>;
-    using T = typename L::type;
     constexpr int kChunk = kThreads * EPT, kGroups = EPT / 8;
-    __shared__ __align__(16) T chunk_mem[kChunk + L::kVec];
-    __shared__ uint64_t list[kList];
-    __shared__ uint64_t scratch64[kThreads / 32];
-    __shared__ float scratch[kThreads / 32];
-    __shared__ uint32_t scratch32[kThreads / 32];
-    __shared__ int list_n;
-
-    const int t = threadIdx.x;
-    const int row = blockIdx.x / p.chunks_per_row, chunk = blockIdx.x - row * p.chunks_per_row;
-    const int first = chunk * kChunk, here = min(kChunk, p.vocab - first);
-    pdl_wait();
-    pdl_trigger();
-    uint8_t* base = p.chunks + static_cast<int64_t>(blockIdx.x) * p.chunk_bytes;
-    ChunkHead* head = reinterpret_cast<ChunkHead*>(base);
-    uint64_t* keys = reinterpret_cast<uint64_t*>(base + sizeof(ChunkHead));
-    // a beam that ended, or that a request does not have yet, is not read
-    const bool live = !(p.ended != nullptr && p.ended[row] != 0) && p.scores[row] > -INFINITY && p.scores[row] < INFINITY;
-    if (!live) {
-        if (t == 0) *head = {0, -INFINITY, 0};
-        if (t < p.select) keys[t] = 0;
-        return;
-    }
-    // ---- the chunk into shared memory, at its own offset from a vector's start ----
-    const T* src = static_cast<const T*>(p.logits) + row * p.row_stride + first;
-    const int skew = VEC ? 0 : static_cast<int>((reinterpret_cast<uintptr_t>(src) & 15u) / sizeof(T));
-    T* mem = chunk_mem + skew;  // element first + i is mem[i]
-    {
-        // whole vectors asynchronously, what is left at the two ends by element
-        const int lead = skew == 0 ? 0 : min(here, L::kVec - skew), vecs = (here - lead) / L::kVec;
-        for (int v = t; v < vecs; v += kThreads) {
-            const int at = lead + v * L::kVec;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(mem + at)),
-                         "l"(reinterpret_cast<uint64_t>(src + at))
-                         : "memory");
-        }
-        if (t < lead) mem[t] = src[t];
-        const int rest = lead + vecs * L::kVec;
-        if (rest + t < here) mem[rest + t] = src[rest + t];
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        __syncthreads();
-    }
+    const int t = threadIdx.x, lane = t & 31;
     // element of group g that comes first, and how far the others are apart
-    auto place = [&](int g, int i) -> int {
+    auto place = [&](int g, int i, int t) -> int {  // of thread t
         if constexpr (VEC) {
             constexpr int kVecs = 8 / L::kVec;  // vectors of a group
             return ((g * kVecs + i / L::kVec) * kThreads + t) * L::kVec + i % L::kVec;
@@ -297,7 +233,7 @@ beam_rows_kernel(const SelectParams p) {
 #pragma unroll
             for (int w = 0; w < 8; w += VEC ? L::kVec : L::kPerWord) {
                 // (these neighbours' bits lie in one word)
-                const int i0 = place(g, w);
+                const int i0 = place(g, w, t);
                 uint32_t on = 0;
                 if (i0 < here) on = bits != nullptr ? __ldg(bits + ((first + i0) >> 5)) >> ((first + i0) & 31) : ~0u;
 #pragma unroll
@@ -313,7 +249,7 @@ beam_rows_kernel(const SelectParams p) {
         if constexpr (VEC) {
 #pragma unroll
             for (int v = 0; v < kGroupWords / 4; ++v) {
-                const uint4 x = *reinterpret_cast<const uint4*>(mem + place(g, v * L::kVec));
+                const uint4 x = *reinterpret_cast<const uint4*>(mem + place(g, v * L::kVec, t));
                 w[4 * v] = x.x;
                 w[4 * v + 1] = x.y;
                 w[4 * v + 2] = x.z;
@@ -323,12 +259,12 @@ beam_rows_kernel(const SelectParams p) {
             const uint32_t* m = reinterpret_cast<const uint32_t*>(chunk_mem + (skew & ~1));
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int at = place(g, 2 * k) / 2;
+                const int at = place(g, 2 * k, t) / 2;
                 w[k] = skew & 1 ? __funnelshift_r(m[at], m[at + 1], 16) : m[at];
             }
         } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) w[k] = mem[place(g, k)];
+            for (int k = 0; k < 8; ++k) w[k] = mem[place(g, k, t)];
         }
     };
     auto element = [&](const uint32_t (&w)[kGroupWords], int i) -> float {
@@ -351,21 +287,21 @@ beam_rows_kernel(const SelectParams p) {
         }
     };
     auto key_of = [&](int g, const uint32_t (&w)[kGroupWords], int i) -> uint64_t {
-        return (static_cast<uint64_t>(order_of(element(w, i))) << 32) | static_cast<uint32_t>(~(first + place(g, i)));
+        return (static_cast<uint64_t>(order_of(element(w, i))) << 32) | static_cast<uint32_t>(~(first + place(g, i, t)));
     };
     // ---- maxima: the thread's, the block's ----
-    float mine = -INFINITY;
-#pragma unroll 4
+    float gmax[kGroups], mine = -INFINITY;
+#pragma unroll
     for (int g = 0; g < kGroups; ++g) {
         uint32_t w[kGroupWords];
         words(g, w);
-        mine = max_nan(mine, largest(w));
+        gmax[g] = largest(w);
+        mine = max_nan(mine, gmax[g]);
     }
     float top = mine;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
     if ((t & 31) == 0) scratch[t >> 5] = top;
-    if (t == 0) list_n = 0;
     __syncthreads();
     top = scratch[0];
 #pragma unroll
@@ -375,40 +311,48 @@ beam_rows_kernel(const SelectParams p) {
         if (t < p.select) keys[t] = 0;
         return;
     }
-    const uint32_t cut = threshold(order_of(mine), order_of(top), p.select, scratch32);
+    const uint32_t cut = threshold<DT == PA_BF16 ? 16 : DT == PA_F16 ? 13 : 0>(order_of(mine), order_of(top), p.select, scratch32);
     const float cut_v = value_of(cut);
     // ---- the list of what reaches the threshold; the sum of the rest ----
-    // exp(x - top): the difference first, which is exact or nearly so (a product with
-    // log2 e first would lose what a large common part of the logits takes)
-    auto exp_of = [&](float x) -> float { return exp2_approx((x - top) * kLog2e); };
-    float2 sum = make_float2(0.f, 0.f);
-#pragma unroll 4
+    // exp(x - top) as 2^(x L - h), L = log2 e and h = top L rounded down: one fused
+    // multiply-add, whose product is exact, so a large common part of the logits takes
+    // nothing; the sum is 2^(top L - h) too large, which is put right below.  (Logits so
+    // large that their differences are zero or past any exponential: zero, what equals
+    // top being in the list.)
+    const bool huge = !(fabsf(top) < 1e30f);
+    const float mult = huge ? 1e-30f : kLog2e, h = huge ? 1e9f : __fmul_rd(top, kLog2e);
+    auto exp_of = [&](float x) -> float { return exp2_approx(fmaf(x, mult, -h)); };
+    float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
     for (int g = 0; g < kGroups; ++g) {
         uint32_t w[kGroupWords];
         words(g, w);
-        if (largest(w) >= cut_v) {
-#pragma unroll 1
-            for (int i = 0; i < 8; ++i) {
-                const float x = value_at<DT>(mem[place(g, i)]);
-                if (x >= cut_v) {
-                    const int at = atomicAdd(&list_n, 1);
-                    if (at < kList)
-                        list[at] = (static_cast<uint64_t>(order_of(x)) << 32) | static_cast<uint32_t>(~(first + place(g, i)));
-                } else {
-                    sum.x += exp_of(x);
-                }
-            }
-        } else {
+        float s[4];
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                float2 e = f2_mul(f2_add(make_float2(element(w, i), element(w, i + 1)), -top), kLog2e);
-                e.x = exp2_approx(e.x);
-                e.y = exp2_approx(e.y);
-                sum = f2_add(sum, e);
+        for (int i = 0; i < 4; ++i) s[i] = exp_of(element(w, 2 * i)) + exp_of(element(w, 2 * i + 1));
+        const bool mixed = gmax[g] >= cut_v;
+        sum0 += mixed ? 0.f : (s[0] + s[1]) + (s[2] + s[3]);
+        // groups that hold one of the list (a few in a hundred): eight lanes take the
+        // eight elements of one
+        for (uint32_t who = __ballot_sync(0xffffffffu, mixed); who != 0; who &= who - 1) {
+            const int at = place(g, lane & 7, (t & ~31) + __ffs(who) - 1);
+            const float x = lane < 8 ? value_at<DT>(mem[at]) : -INFINITY;
+            if (x >= cut_v) {
+                const int n = atomicAdd(&list_n, 1);
+                if (n < kList) list[n] = (static_cast<uint64_t>(order_of(x)) << 32) | static_cast<uint32_t>(~(first + at));
+            } else {
+                sum1 += exp_of(x);
             }
         }
     }
-    uint64_t units = static_cast<uint64_t>(__float2ll_rn((sum.x + sum.y) * 1099511627776.f));
+    // 1 - 2^-(top L - h), to a few times its own 2^-24
+    const float u = huge ? 0.f : fmaf(top, kLog2e, -h) * static_cast<float>(kLn2);
+    const float over = u * fmaf(u, fmaf(u, fmaf(u, fmaf(u, 1.f / 120.f, -1.f / 24.f), 1.f / 6.f), -0.5f), 1.f);
+    auto units_of = [&](float x) -> uint64_t {
+        const float y = x * 1099511627776.f;
+        return static_cast<uint64_t>(__float2ll_rn(y) - __float2ll_rn(y * over));
+    };
+    uint64_t units = units_of(sum0 + sum1);
     __syncthreads();
     const int n = list_n;
     if (n <= kList) {
@@ -460,11 +404,73 @@ beam_rows_kernel(const SelectParams p) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 if (element(w, i) > -INFINITY && key_of(g, w, i) < last)
-                    units += static_cast<uint64_t>(__float2ll_rn(exp_of(element(w, i)) * 1099511627776.f));
+                    units += units_of(huge ? (element(w, i) == top ? 1.f : 0.f) : exp_of(element(w, i)));
         }
     }
     units = block_sum(units, scratch64);
     if (t == 0) *head = {units, top, 0};
+}
+
+// EPT elements a thread, in groups of eight.  VEC: every row is 16-byte aligned and a group
+// is whole vectors of shared memory; otherwise it is four words' pairs of 16-bit elements
+// (eight floats), which lie in shared memory as they lie in memory, up to 14 bytes behind
+// a vector's start.  Which element goes to which thread does not depend on a row's
+// address, so equal rows get equal sums.
+template <int DT, int EPT, bool VEC>
+__global__ void __launch_bounds__(kThreads)
+beam_rows_kernel(const SelectParams p) {
+    using L = Logits<DT>;
+    using T = typename L::type;
+    constexpr int kChunk = kThreads * EPT;
+    extern __shared__ __align__(16) uint8_t dynamic[];  // [kChunk + kVec] T
+    __shared__ uint64_t list[kList];
+    __shared__ uint64_t scratch64[kThreads / 32];
+    __shared__ float scratch[kThreads / 32];
+    __shared__ uint32_t scratch32[kThreads / 32];
+    __shared__ uint64_t full;
+    __shared__ int list_n, abort_flag;
+
+    const int t = threadIdx.x;
+    const int row = blockIdx.x / p.chunks_per_row, first = (blockIdx.x - row * p.chunks_per_row) * kChunk;
+    const int here = min(kChunk, p.vocab - first);
+    if (t == 0) {
+        mbar_init(smem_addr(&full), 1);
+        list_n = 0;
+        abort_flag = 0;
+        fence_mbar_init();
+    }
+    pdl_wait();
+    pdl_trigger();
+    ChunkHead* head = p.heads + blockIdx.x;
+    uint64_t* keys = p.keys + static_cast<int64_t>(blockIdx.x) * p.select;
+    // a beam that ended, or that a request does not have yet, is not read
+    const bool live = !(p.ended != nullptr && p.ended[row] != 0) && p.scores[row] > -INFINITY && p.scores[row] < INFINITY;
+    if (!live) {
+        if (t == 0) *head = {0, -INFINITY, 0};
+        if (t < p.select) keys[t] = 0;
+        return;
+    }
+    // the chunk into shared memory, at its own offset from a vector's start: whole
+    // vectors by one bulk copy, the up to 7 elements before and behind them by element
+    const T* src = static_cast<const T*>(p.logits) + row * p.row_stride + first;
+    const int skew = VEC ? 0 : static_cast<int>((reinterpret_cast<uintptr_t>(src) & 15u) / sizeof(T));
+    T* mem = reinterpret_cast<T*>(dynamic) + skew;  // element first + i is mem[i]
+    const int lead = skew == 0 ? 0 : min(here, L::kVec - skew), vecs = (here - lead) / L::kVec;
+    if (t == 0) {
+        if (vecs > 0) {
+            mbar_expect_tx(smem_addr(&full), vecs * 16);
+            bulk_g2s_hint(smem_addr(mem + lead), src + lead, vecs * 16, smem_addr(&full), policy_evict_first());
+        } else {
+            mbar_arrive(smem_addr(&full));
+        }
+    }
+    if (t < lead) mem[t] = src[t];
+    if (lead + vecs * L::kVec + t < here) mem[lead + vecs * L::kVec + t] = src[lead + vecs * L::kVec + t];
+    __syncthreads();  // (the barrier's initialisation, the single elements)
+    // (one outcome for the block: a wait that ran out ends it)
+    if (__syncthreads_or(!mbar_wait(smem_addr(&full), 0u, p.status, &abort_flag))) return;
+    rows_chunk<DT, EPT, VEC>(p, mem, reinterpret_cast<T*>(dynamic), skew, first, here, row, head, keys, list, list_n, scratch64,
+                             scratch, scratch32);
 }
 
 // A number as the sum of two floats, hi the sum rounded: 48 bits.  Below binary32's range
@@ -481,6 +487,20 @@ __device__ __forceinline__ Two two_add(Two a, Two b) {
     if (!(s.hi > -INFINITY)) return s;
     s.lo += a.lo + b.lo;
     return two_sum(s.hi, s.lo);
+}
+
+// log(units 2^-40), units >= 2^40 or a little less, to about 2^-29: the power of two apart,
+// then log m = y + (m exp(-y) - 1) for y the binary32 logarithm
+__device__ __forceinline__ Two log_units(uint64_t units) {
+    const int k = 23 - __clzll(static_cast<int64_t>(units));  // units = m 2^k, m in [2^40, 2^41)
+    const uint64_t m = k >= 0 ? units >> k : units << -k;
+    const float y = __logf(static_cast<float>(m) * 9.094947017729282e-13f);  // (2^-40)
+    const uint64_t e = exp_units(-y, 0.f);
+    const int64_t more = static_cast<int64_t>((__umul64hi(m, e) << 24) | (m * e >> 40)) - (1ll << 40);
+    const float f = static_cast<float>(k);
+    // k ln 2 in the same three terms, the first two exact
+    const Two a = two_sum(f * kLn2a, f * kLn2b);
+    return two_add(two_add(a, {f * kLn2c, 0.f}), two_sum(y, static_cast<float>(more) * 9.094947017729282e-13f));
 }
 
 struct Candidate {
@@ -515,100 +535,88 @@ beam_requests_kernel(const SelectParams p) {
         if (t == 0) report(p.status, PA_ERR_INVALID_ARG);
         r0 = r1 = 0;
     }
-    auto head_of = [&](int row, int c) -> const uint8_t* {
-        return p.chunks + (static_cast<int64_t>(row) * S + c) * p.chunk_bytes;
-    };
     if (t == 0) list_n = 0;
-    // ---- each row's log-sum-exp: a warp takes a row, then a thread its logarithm ----
     RowSum* sums = r1 - r0 <= kRowsHere ? row_sums : p.sums + r0;
+    // a key's candidate: score + ((x - top) - log)
+    auto scored = [&](int row, float score, const RowSum& sum, uint64_t key) -> Candidate {
+        const float x = value_of(static_cast<uint32_t>(key >> 32));
+        return {two_add(two_add(two_sum(x, -sum.top), {-sum.log_h, -sum.log_l}), {score, 0.f}), key, row};
+    };
+    // (the score's float keeps the scores' order, so it serves as the threshold's key)
+    auto order = [](const Candidate& c) -> uint32_t { return order_of(fmaxf(c.s.hi, -3.4028234e38f)); };
+    // use(candidate) for all that this thread looks at.  A warp takes a row, or, of few
+    // rows, several warps do.
+    const int per_row = S * K, sharers = max(1, min(kThreads / 32, kThreads / 32 / max(r1 - r0, 1)));
+    auto candidates = [&](auto use) {
+        for (int row = r0 + warp / sharers; row < r1 && warp / sharers < kThreads / 32 / sharers;
+             row += kThreads / 32 / sharers) {
+            const float score = p.scores[row];
+            if (!(score > -INFINITY && score < INFINITY)) continue;
+            const int first = (warp % sharers) * 32 + lane;
+            if (p.ended != nullptr && p.ended[row] != 0) {
+                if (first == 0) use(Candidate{{score, 0.f}, static_cast<uint32_t>(~p.end_token), row});
+                continue;
+            }
+            const RowSum sum = sums[row - r0];
+            if (sum.log_h == INFINITY) continue;
+            const uint64_t* keys = p.keys + static_cast<int64_t>(row) * per_row;
+            for (int i = first; i < per_row; i += 32 * sharers)
+                if (keys[i] != 0) use(scored(row, score, sum, keys[i]));
+        }
+    };
+    // ---- each row's log-sum-exp, by a warp ----
     for (int row = r0 + warp; row < r1; row += kThreads / 32) {
         const float score = p.scores[row];
         if (!(score < INFINITY) && lane == 0) report(p.status, PA_ERR_INVALID_ARG);
+        const ChunkHead* heads = p.heads + static_cast<int64_t>(row) * S;
+        const uint64_t* keys = p.keys + static_cast<int64_t>(row) * per_row;
         float top = -INFINITY;
         bool bad = false;
         for (int c = lane; c < S; c += 32) {
-            const ChunkHead h = *reinterpret_cast<const ChunkHead*>(head_of(row, c));
-            top = fmaxf(top, h.top);
-            bad |= h.bad != 0;
+            top = fmaxf(top, heads[c].top);
+            bad |= heads[c].bad != 0;
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         bad = __any_sync(0xffffffffu, bad);
         if (bad && lane == 0) report(p.status, PA_ERR_INVALID_ARG);
-        uint64_t units = 0;
+        RowSum sum{top, INFINITY, 0.f, 0};
         if (!bad && top > -INFINITY) {
-            for (int i = lane; i < S * K; i += 32) {
-                const int c = i / K;
-                const uint64_t k = reinterpret_cast<const uint64_t*>(head_of(row, c) + sizeof(ChunkHead))[i - c * K];
+            uint64_t units = 0;
+#pragma unroll 4
+            for (int i = lane; i < per_row; i += 32) {
+                const uint64_t k = keys[i];
                 if (k != 0) units += exp_units(value_of(static_cast<uint32_t>(k >> 32)), top);
             }
             // (a chunk's units count against its own maximum)
             for (int c = lane; c < S; c += 32) {
-                const ChunkHead h = *reinterpret_cast<const ChunkHead*>(head_of(row, c));
-                const uint64_t e = h.sum != 0 ? exp_units(h.top, top) : 0;
-                units += (__umul64hi(h.sum, e) << 24) | (h.sum * e >> 40);
+                const uint64_t u = heads[c].sum, e = u != 0 ? exp_units(heads[c].top, top) : 0;
+                units += (__umul64hi(u, e) << 24) | (u * e >> 40);
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) units += __shfl_xor_sync(0xffffffffu, units, o);
+            const Two l = log_units(units);
+            sum.log_h = l.hi;
+            sum.log_l = l.lo;
         }
-        if (lane == 0) {
-            // (the units wait where the logarithm goes)
-            sums[row - r0].top = top;
-            sums[row - r0].log_h = __uint_as_float(static_cast<uint32_t>(units));
-            sums[row - r0].log_l = __uint_as_float(static_cast<uint32_t>(units >> 32));
-        }
+        if (lane == 0) sums[row - r0] = sum;
     }
     __syncthreads();
-    for (int r = t; r < r1 - r0; r += kThreads) {
-        const uint64_t units =
-            __float_as_uint(sums[r].log_h) | static_cast<uint64_t>(__float_as_uint(sums[r].log_l)) << 32;
-        const double l = units != 0 ? log(static_cast<double>(units) * kUnit) : 0.0;
-        sums[r].log_h = units != 0 ? static_cast<float>(l) : INFINITY;
-        sums[r].log_l = static_cast<float>(l - static_cast<float>(l));
-    }
-    __syncthreads();
-    // ---- candidates: slot i of the request's (row, chunk, rank); an ended row has one ----
-    const int64_t per_row = static_cast<int64_t>(S) * K, total = (r1 - r0) * per_row;
-    auto candidate = [&](int64_t i, Candidate& c) -> bool {
-        c.row = r0 + static_cast<int>(i / per_row);
-        const int j = static_cast<int>(i - (c.row - r0) * per_row);
-        const float score = p.scores[c.row];
-        if (!(score > -INFINITY && score < INFINITY)) return false;
-        if (p.ended != nullptr && p.ended[c.row] != 0) {
-            c.s = {score, 0.f};
-            c.key = static_cast<uint32_t>(~p.end_token);
-            return j == 0;
-        }
-        const int chunk = j / K;
-        c.key = reinterpret_cast<const uint64_t*>(head_of(c.row, chunk) + sizeof(ChunkHead))[j - chunk * K];
-        const RowSum sum = sums[c.row - r0];
-        if (c.key == 0 || sum.log_h == INFINITY) return false;
-        // score + ((x - top) - log)
-        const float x = value_of(static_cast<uint32_t>(c.key >> 32));
-        c.s = two_add(two_add(two_sum(x, -sum.top), {-sum.log_h, -sum.log_l}), {score, 0.f});
-        return true;
-    };
-    // (the score's float keeps the scores' order, so it serves as the threshold's key)
-    auto key_of = [](Two s) -> uint32_t { return order_of(fmaxf(s.hi, -3.4028234e38f)); };
+    // ---- the K best of all candidates ----
     uint32_t mine = kNothing;
-    for (int64_t i = t; i < total; i += kThreads) {
-        Candidate c;
-        if (candidate(i, c)) mine = max(mine, key_of(c.s));
-    }
+    candidates([&](const Candidate& c) { mine = max(mine, order(c)); });
     uint32_t top = __reduce_max_sync(0xffffffffu, mine);
     if (lane == 0) scratch[warp] = top;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) top = max(top, scratch[w]);
-    const uint32_t cut = top == kNothing ? kNothing + 1 : threshold(mine, top, K, scratch);
-    if (mine >= cut) {
-        for (int64_t i = t; i < total; i += kThreads) {
-            Candidate c;
-            if (candidate(i, c) && key_of(c.s) >= cut) {
-                const int n = atomicAdd(&list_n, 1);
-                if (n < kList) list[n] = c;
-            }
-        }
+    const uint32_t cut = top == kNothing ? kNothing + 1 : threshold<0>(mine, top, K, scratch);
+    if (__any_sync(0xffffffffu, mine >= cut)) {
+        candidates([&](const Candidate& c) {
+            if (order(c) < cut) return;
+            const int n = atomicAdd(&list_n, 1);
+            if (n < kList) list[n] = c;
+        });
     }
     __syncthreads();
     const int n = list_n;
@@ -632,10 +640,9 @@ beam_requests_kernel(const SelectParams p) {
     Candidate last{{INFINITY, 0.f}, 0, -1};
     for (int r = 0; r < K; ++r) {
         Candidate best = none;
-        for (int64_t i = t; i < total; i += kThreads) {
-            Candidate c;
-            if (candidate(i, c) && before(last, c) && (best.row < 0 || before(c, best))) best = c;
-        }
+        candidates([&](const Candidate& c) {
+            if (before(last, c) && (best.row < 0 || before(c, best))) best = c;
+        });
         auto join = [&](const Candidate& c) {
             if (c.row >= 0 && (best.row < 0 || before(c, best))) best = c;
         };
@@ -656,24 +663,30 @@ beam_requests_kernel(const SelectParams p) {
     }
 }
 
-// Elements a thread holds.  More make longer loads and fewer lists; a small batch
-// takes fewer, so that its chunks reach every SM.
+// Elements a thread holds: more of them share a chunk's threshold and list (some 2700
+// instructions), fewer keep more blocks on an SM (512 rows of 128256 bf16: 64 elements
+// 40.5 us, 128 elements 43.1) and reach every SM with a small batch.
 int chunk_elems(int64_t rows, int vocab, int dtype, int sms) {
-    const int most = dtype == PA_F32 ? 32 : 64;
-    int ept = most;
+    int ept = dtype == PA_F32 ? 32 : 64;
     while (ept > 8 && rows * ((vocab + kThreads * ept - 1) / (kThreads * ept)) < 2ll * sms) ept /= 2;
     return ept;
 }
 int chunks_of(int vocab, int ept) { return (vocab + kThreads * ept - 1) / (kThreads * ept); }
-int64_t chunk_bytes(int select) { return static_cast<int64_t>(sizeof(ChunkHead)) + 8ll * select; }
 
+template <int DT, int EPT, bool VEC>
+cudaError_t launch_rows_of(const SelectParams& p, int items, cudaStream_t s) {
+    const int smem = (kThreads * EPT + Logits<DT>::kVec) * static_cast<int>(sizeof(typename Logits<DT>::type));
+    static LaunchCache cache;
+    if (blocks_per_sm(beam_rows_kernel<DT, EPT, VEC>, kThreads, smem, cache) <= 0) return cudaErrorUnknown;
+    return launch_pdl(beam_rows_kernel<DT, EPT, VEC>, items, kThreads, smem, s, p);
+}
 template <int DT, bool VEC>
-cudaError_t launch_rows(const SelectParams& p, int ept, int grid, cudaStream_t s) {
-    if (ept == 8) return launch_pdl(beam_rows_kernel<DT, 8, VEC>, grid, kThreads, 0, s, p);
-    if (ept == 16) return launch_pdl(beam_rows_kernel<DT, 16, VEC>, grid, kThreads, 0, s, p);
+cudaError_t launch_rows(const SelectParams& p, int ept, int items, cudaStream_t s) {
     if constexpr (DT != PA_F32)
-        if (ept == 64) return launch_pdl(beam_rows_kernel<DT, 64, VEC>, grid, kThreads, 0, s, p);
-    return launch_pdl(beam_rows_kernel<DT, 32, VEC>, grid, kThreads, 0, s, p);
+        if (ept == 64) return launch_rows_of<DT, 64, VEC>(p, items, s);
+    if (ept == 32) return launch_rows_of<DT, 32, VEC>(p, items, s);
+    if (ept == 16) return launch_rows_of<DT, 16, VEC>(p, items, s);
+    return launch_rows_of<DT, 8, VEC>(p, items, s);
 }
 
 }  // namespace
@@ -685,7 +698,7 @@ extern "C" size_t pa_beam_select_workspace_size(int32_t num_rows, int32_t vocab,
     if (num_rows <= 0 || vocab <= 0 || num_select <= 0 || num_select > kMaxSelect) return 0;
     // (for the shortest chunks, which any device may take)
     const size_t chunks = static_cast<size_t>(num_rows) * chunks_of(vocab, 8);
-    return static_cast<size_t>(num_rows) * sizeof(RowSum) + chunks * chunk_bytes(num_select);
+    return static_cast<size_t>(num_rows) * sizeof(RowSum) + chunks * (sizeof(ChunkHead) + 8 * static_cast<size_t>(num_select));
 }
 
 extern "C" pa_status pa_beam_select(float* scores_out, int32_t* rows_out, int32_t* tokens_out, const void* logits,
@@ -721,8 +734,6 @@ extern "C" pa_status pa_beam_select(float* scores_out, int32_t* rows_out, int32_
     p.allowed = allowed;
     p.ended = ended;
     p.status = dev_status;
-    p.sums = static_cast<RowSum*>(workspace);
-    p.chunks = static_cast<uint8_t*>(workspace) + static_cast<size_t>(num_rows) * sizeof(RowSum);
     p.row_stride = row_stride;
     p.allowed_stride = allowed_stride;
     p.vocab = vocab;
@@ -732,11 +743,13 @@ extern "C" pa_status pa_beam_select(float* scores_out, int32_t* rows_out, int32_
     p.end_token = end_token;
     const int ept = chunk_elems(num_rows, vocab, dtype, sms);
     p.chunks_per_row = chunks_of(vocab, ept);
-    p.chunk_bytes = static_cast<int32_t>(chunk_bytes(num_select));
+    p.sums = static_cast<RowSum*>(workspace);
+    p.heads = reinterpret_cast<ChunkHead*>(p.sums + num_rows);
+    p.keys = reinterpret_cast<uint64_t*>(p.heads + static_cast<int64_t>(num_rows) * p.chunks_per_row);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (num_rows > 0) {
         const int64_t grid = static_cast<int64_t>(num_rows) * p.chunks_per_row;
-        if (grid > INT32_MAX) return PA_ERR_UNSUPPORTED;
+        if (grid > INT32_MAX / 2) return PA_ERR_UNSUPPORTED;
         const bool vec = (reinterpret_cast<uintptr_t>(logits) & 15u) == 0 && (row_stride * bytes) % 16 == 0;
         const int g = static_cast<int>(grid);
         cudaError_t e;

@@ -80,6 +80,7 @@ struct CascadeParams {
     int32_t part;       // keys of a part (a multiple of kBN)
     int32_t max_parts;
     int32_t own;        // the sequences' own keys too, or the prefixes alone
+    int32_t stack;      // groups share; 0: every sequence's keys are one segment
     int32_t order_cap;  // entries the shared-memory work order holds (set by the launch)
     float scale_log2;   // scale * log2(e)
 };
@@ -110,7 +111,7 @@ __device__ __forceinline__ Group group_at(const CascadeParams& p, int g) {
            r.s0 <= p.max_shared && r.s0 % p.block_size == 0 &&
            static_cast<int64_t>(r.s0) <= static_cast<int64_t>(p.max_blocks) * p.block_size;
     // (a group of one: its prefix and its own keys are one segment)
-    r.shares = r.ok && r.s0 > 0 && (r.b1 - r.b0 > 1 || !p.own);
+    r.shares = r.ok && p.stack && r.s0 > 0 && (r.b1 - r.b0 > 1 || !p.own);
     return r;
 }
 // the group of sequence b (the last whose first sequence is not behind it)
@@ -684,10 +685,10 @@ cascade_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
             return stop != 0;
         };
         bool stop = false;
-        const int t_row = r / p.group, g_row = r - t_row * p.group;
         // where this row of item w goes: its offset in out (>= 0), or -2 - its slot in
         // the workspace, or -1 for no row
         auto row_of = [&](const Work& w) -> int64_t {
+            const int t_row = r / p.group, g_row = r - t_row * p.group;
             if (t_row >= w.ntok) return -1;
             const int64_t row = static_cast<int64_t>(w.tok0 + t_row) * p.num_heads + w.kvh * p.group + g_row;
             return w.part < 0 ? row * kD : -2 - (row * p.max_parts + w.part);
@@ -769,9 +770,10 @@ cascade_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
             if (end && !pend) break;
             const Work w = end ? Work{} : item_work(rnd, item);
             const int ntiles = w.tiles();
-            const bool row_valid = t_row < w.ntok;
             const int64_t row_off = row_of(w);
-            const int lim = min(w.nkeys, w.shift + t_row + 1);  // visible keys of this row: [0, lim)
+            const int t_row = r / p.group;
+            // visible keys of this row: [0, lim)
+            const int lim = t_row < w.ntok ? min(w.nkeys, w.shift + t_row + 1) : 0;
             if (ntiles == 0 && !end) {
                 // no visible key for any row of the item: output 0 (a part: the merge
                 // does not read it)
@@ -797,7 +799,7 @@ cascade_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                 if (t >= ntiles) break;
                 const int b = t & 1;
                 const int key0 = t * kBN + 64 * x;  // first key of this thread's 64 columns
-                const int vis = row_valid ? lim - key0 : 0;  // visible keys of these columns: [0, vis)
+                const int vis = lim - key0;  // visible keys of these columns: [0, vis)
                 ok = ok && mbar_wait(s_full + 8 * b, s_use[b] & 1u, p.status, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 tc_fence_after();  // for both reads of S below
@@ -1018,26 +1020,53 @@ __global__ void __launch_bounds__(256) cascade_merge_kernel(const CascadeParams 
         make_uint2(pack2<DT>(acc.x * inv, acc.y * inv), pack2<DT>(acc.z * inv, acc.w * inv));
 }
 
-// Keys of a part.  Long ones have less to merge; the items (query tiles, parts, KV heads) have
-// to reach all SMs several times over.  For a GB300's SMs whatever the device, so that
-// the workspace query needs none.
+// The SMs of a GB300, whatever the device: the workspace query needs none.
 constexpr int kSms = 152;
-int part_keys(int64_t tiles, int max_keys) {
-    int part = 256;
-    while (part < max_keys && tiles * ((max_keys + 2 * part - 1) / (2 * part)) >= 3 * kSms) part *= 2;
-    return part;
-}
 
 struct Plan {
+    bool stack;
     int part, max_parts;
     size_t o_off, bytes;
 };
-Plan plan_of(int64_t num_seqs, int64_t total_q, int num_heads, int num_kv_heads, int max_q, int max_k, int max_shared) {
+
+// How the batch is cut, from what the host knows of it.
+//
+// Stacking.  Sequences whose queries fill two tiles or more each gain little from standing
+// together, and their rows' parts cost a write, a read and a merge: they take their keys as
+// one segment straight to out.  (Four system prompts of 1024 to 8192 tokens, 20 prompts of
+// 16 to 1024 tokens behind them, 32/8 heads, bf16: PLAN_PROMPTS_STACKED us stacked, PLAN_PROMPTS
+// not.)  With few query tiles over long keys they are cut into parts all the same.
+//
+// Parts.  n parts of the longest prefix make tiles * n items for the SMs' rounds; an item
+// costs its key tiles and some 2.5 more for its start and end, a part's rows 1 KB of traffic
+// a row and head.  The n with the least such time is taken.
+Plan plan_of(int64_t num_seqs, int64_t total_q, int num_heads, int num_kv_heads, int max_k, int max_shared) {
     Plan r;
     const int group = num_heads / num_kv_heads;
     const int64_t tiles = (total_q * group + kRows - 1) / kRows * num_kv_heads;
-    r.part = part_keys(tiles < 1 ? 1 : tiles, max_shared > 0 ? max_shared : max_k);
-    r.max_parts = (max_k + r.part - 1) / r.part + 1;
+    r.stack = max_shared > 0 && total_q * group < 2ll * kRows * num_seqs;
+    const int keys = r.stack ? max_shared : max_k;
+    const double rows_us = static_cast<double>(total_q) * num_heads * 1032.0 / 6.5e6;  // a part's traffic
+    double best = 0.0;
+    r.part = kBN;
+    for (int n = 1; n <= 64; ++n) {
+        int part = ((keys + n - 1) / n + kBN - 1) / kBN * kBN;
+        if (part < 2 * kBN) part = 2 * kBN;
+        const double item = 1.3 * (part / kBN + 2.5), items = static_cast<double>(tiles) * n;
+        const double rounds = std::ceil(items / kSms);
+        const double t = rounds * item + (n > 1 || r.stack ? (n + 1) * rows_us : 0.0);
+        if (n == 1 || t < best) {
+            best = t;
+            r.part = part;
+        }
+        if (part == 2 * kBN) break;
+    }
+    // (not stacked and one part: everything goes straight to out)
+    r.max_parts = !r.stack && max_k <= r.part ? 1 : (max_k + r.part - 1) / r.part + 1;
+    if (r.max_parts == 1) {
+        r.o_off = r.bytes = 0;
+        return r;
+    }
     const size_t rows = static_cast<size_t>(total_q) * num_heads * r.max_parts;
     r.o_off = (rows * 4 + 255) & ~static_cast<size_t>(255);
     r.bytes = r.o_off + rows * kD * 4 + 16;  // (32-byte stores: the pointer is rounded up)
@@ -1065,6 +1094,7 @@ pa_status launch_cascade(CascadeParams p, const CUtensorMap& map_k, const CUtens
     const int64_t cap = static_cast<int64_t>(device_sm_count()) * per_sm;
     const int grid = static_cast<int>(max_items < cap ? max_items : cap);
     if (grid > 0 && launch_pdl(kern, grid, kThreads, smem, stream, map_k, map_v, map_q, p) != cudaSuccess) return PA_ERR_CUDA;
+    if (p.max_parts == 1) return PA_OK;
     const int64_t per_seq = (static_cast<int64_t>(p.max_q) * p.num_heads + 7) / 8;
     if (per_seq > INT32_MAX) return PA_ERR_UNSUPPORTED;
     const dim3 mgrid(static_cast<unsigned>(per_seq), static_cast<unsigned>(p.num_seqs));
@@ -1082,7 +1112,7 @@ extern "C" size_t pa_varlen_cascade_workspace_size(int32_t num_seqs, int64_t tot
     if (num_seqs <= 0 || total_q <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads != 0 ||
         head_size <= 0 || max_seqlen_q <= 0 || max_seqlen_k < 0 || max_shared_len < 0 || block_size <= 0)
         return 0;
-    return plan_of(num_seqs, total_q, num_heads, num_kv_heads, max_seqlen_q, max_seqlen_k, max_shared_len).bytes;
+    return plan_of(num_seqs, total_q, num_heads, num_kv_heads, max_seqlen_k, max_shared_len).bytes;
 }
 
 extern "C" pa_status pa_varlen_cascade(void* out, const void* q, pa_dtype q_dtype, const pa_kv_cache* cache,
@@ -1117,8 +1147,8 @@ extern "C" pa_status pa_varlen_cascade(void* out, const void* q, pa_dtype q_dtyp
     if (static_cast<int64_t>(num_seqs) + num_groups > kMaxSegments) return PA_ERR_UNSUPPORTED;
     const int64_t rows = cache->num_blocks * cache->num_kv_heads * bs;
     if (rows > INT32_MAX || total_q > INT32_MAX - kRows) return PA_ERR_UNSUPPORTED;
-    const Plan plan = plan_of(num_seqs, total_q, num_heads, cache->num_kv_heads, max_seqlen_q, max_seqlen_k, max_shared_len);
-    if (workspace == nullptr || workspace_bytes < plan.bytes || (reinterpret_cast<uintptr_t>(workspace) & 15u))
+    const Plan plan = plan_of(num_seqs, total_q, num_heads, cache->num_kv_heads, max_seqlen_k, max_shared_len);
+    if (plan.bytes > 0 && (workspace == nullptr || workspace_bytes < plan.bytes || (reinterpret_cast<uintptr_t>(workspace) & 15u)))
         return PA_ERR_INVALID_ARG;
 
     CascadeParams p{};
@@ -1150,6 +1180,7 @@ extern "C" pa_status pa_varlen_cascade(void* out, const void* q, pa_dtype q_dtyp
     p.part = plan.part;
     p.max_parts = plan.max_parts;
     p.own = 1;
+    p.stack = plan.stack ? 1 : 0;
     p.scale_log2 = scale * 1.4426950408889634f;
     CUtensorMap map_k, map_v, map_q;
     if (!make_cache_map(&map_k, cache->k_cache, rows, q_dtype, bs) ||

@@ -1,6 +1,7 @@
 // CPython module _native: the argument checks and the marshalling of the calls
-// that a decode step makes once a layer (pa_qk_norm_rope, pa_qk_norm_rope_write,
-// pa_decode_window, pa_prefill_varlen_window).  The same as a ctypes call would do,
+// that a decode step makes (once a layer pa_qk_norm_rope, pa_qk_norm_rope_write,
+// pa_decode_window, pa_prefill_varlen_window, pa_varlen_cascade; once pa_beam_select,
+// pa_beam_reorder).  The same as a ctypes call would do,
 // in a third of the time: through ctypes the checks and conversions took 8 of the 11
 // microseconds of a small call.
 //
@@ -22,6 +23,11 @@ decltype(&pa_qk_norm_rope) c_rope;
 decltype(&pa_qk_norm_rope_write) c_write;
 decltype(&pa_decode_window) c_decode;
 decltype(&pa_prefill_varlen_window) c_prefill;
+// set by setup_beams(), with torch's types of what ended
+decltype(&pa_varlen_cascade) c_cascade;
+decltype(&pa_beam_select) c_select;
+decltype(&pa_beam_reorder) c_reorder;
+PyObject *t_u8, *t_bool;
 
 struct Tensor {
     Py_ssize_t dim;
@@ -392,6 +398,192 @@ PyObject* prefill_varlen_window(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// contiguous, of that type and shape: n1 < 0 a vector, -2 in n0 any length
+bool exact(PyObject* o, const char* name, int64_t* index, PyObject* dtype, int64_t n0, int64_t n1, Tensor* t) {
+    if (!load(o, name, index, t)) return false;
+    if (t->dtype != dtype) {
+        PyErr_Format(PyExc_TypeError, "%s must be %R, got %R", name, dtype, t->dtype);
+        return false;
+    }
+    if (t->dim != (n1 < 0 ? 1 : 2) || (n0 >= 0 && t->size[0] != n0) || (n1 >= 0 && t->size[1] != n1)) {
+        if (n1 < 0) PyErr_Format(PyExc_ValueError, "%s must have %lld entries", name, static_cast<long long>(n0));
+        else PyErr_Format(PyExc_ValueError, "%s must be [%lld, %lld]", name, static_cast<long long>(n0),
+                          static_cast<long long>(n1));
+        return false;
+    }
+    return true;
+}
+
+bool workspace_of(PyObject* o, int64_t* index, void** ptr, int64_t* bytes) {
+    *ptr = nullptr;
+    *bytes = 0;
+    if (o == Py_None) return true;
+    Tensor t;
+    int64_t elem;
+    if (!load(o, "workspace", index, &t) || !call_int(o, n_numel, bytes) || !call_int(o, n_element_size, &elem)) return false;
+    *ptr = t.ptr;
+    *bytes *= elem;
+    return true;
+}
+
+bool fits32(int64_t n, const char* name) {
+    if (n <= INT32_MAX) return true;
+    PyErr_Format(PyExc_ValueError, "%s is too large", name);
+    return false;
+}
+
+// (out, q, k_cache, v_cache, k_scale, v_scale, block_table, cu_seq_lens_q, cu_seq_lens_k, max_seqlen_q,
+// max_seqlen_k, scale, cu_groups, shared_lens, max_group_size, max_shared_len, workspace, dev_status)
+PyObject* varlen_cascade(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    int64_t dev = -1, max_q, max_k, max_group, max_shared, ws_bytes;
+    Tensor q, out, table, cu_q, cu_k, cu_g, shared;
+    pa_dtype dt;
+    pa_kv_cache c;
+    float scale;
+    int32_t* status;
+    void* ws;
+    if (!count(n, 18) || !load(a[1], "q", &dev, &q) || !load(a[0], "out", &dev, &out)) return nullptr;
+    if (out.dtype != q.dtype) {
+        PyErr_Format(PyExc_TypeError, "out must be %R, got %R", q.dtype, out.dtype);
+        return nullptr;
+    }
+    if (!queries(a[0], a[1], a + 2, &dev, &q, &out, &dt, &c) ||
+        !exact(a[7], "cu_seq_lens_q", &dev, t_i32, -2, -1, &cu_q) || !exact(a[13], "shared_lens", &dev, t_i32, -2, -1, &shared))
+        return nullptr;
+    if (cu_q.size[0] < 1) {
+        PyErr_SetString(PyExc_ValueError, "cu_seq_lens_q must have num_seqs + 1 entries");
+        return nullptr;
+    }
+    if (!fits32(cu_q.size[0], "the batch") || !exact(a[8], "cu_seq_lens_k", &dev, t_i32, cu_q.size[0], -1, &cu_k) ||
+        !load_as(a[6], "block_table", &dev, t_i32, cu_q.size[0] - 1, 0, &table) ||
+        !exact(a[12], "cu_groups", &dev, t_i32, shared.size[0] + 1, -1, &cu_g) || !as_int(a[9], &max_q) ||
+        !as_int(a[10], &max_k) || !as_float(a[11], &scale) || !as_int(a[14], &max_group) || !as_int(a[15], &max_shared) ||
+        !workspace_of(a[16], &dev, &ws, &ws_bytes) || !status_of(a[17], &dev, &status))
+        return nullptr;
+    return on_device(dev, [&](pa_stream_t s) {
+        return c_cascade(out.ptr, q.ptr, dt, &c, static_cast<const int32_t*>(table.ptr), static_cast<int32_t>(table.size[1]),
+                         static_cast<const int32_t*>(cu_q.ptr), static_cast<const int32_t*>(cu_k.ptr),
+                         static_cast<int32_t>(cu_q.size[0] - 1), q.size[0], static_cast<int32_t>(max_q),
+                         static_cast<int32_t>(max_k), static_cast<int32_t>(q.size[1]), scale,
+                         static_cast<const int32_t*>(cu_g.ptr), static_cast<const int32_t*>(shared.ptr),
+                         static_cast<int32_t>(shared.size[0]), static_cast<int32_t>(max_group),
+                         static_cast<int32_t>(max_shared), ws, static_cast<size_t>(ws_bytes), status, s);
+    });
+}
+
+// (scores_out, rows_out, tokens_out, logits, scores, cu_beams, allowed, ended, end_token, workspace, dev_status)
+PyObject* beam_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    int64_t dev = -1, stride[4], end_token, ws_bytes;
+    Tensor x, scores, cu, so, ro, to, allowed{}, ended{};
+    int32_t* status;
+    void* ws;
+    if (!count(n, 11) || !load(a[3], "logits", &dev, &x, stride)) return nullptr;
+    pa_dtype dt;
+    if (x.dtype == t_f32) dt = PA_F32;
+    else if (x.dtype == t_f16) dt = PA_F16;
+    else if (x.dtype == t_bf16) dt = PA_BF16;
+    else {
+        PyErr_Format(PyExc_TypeError, "unsupported dtype %R", x.dtype);
+        return nullptr;
+    }
+    if (x.dim != 2 || (x.size[1] > 1 && stride[1] != 1)) {
+        PyErr_SetString(PyExc_ValueError, "logits must be [num_rows, vocab], the tokens of a row contiguous");
+        return nullptr;
+    }
+    const int64_t R = x.size[0], V = x.size[1], words = (V + 31) / 32;
+    if (!fits32(R, "num_rows") || !fits32(V, "vocab") || !exact(a[5], "cu_beams", &dev, t_i32, -2, -1, &cu)) return nullptr;
+    const int64_t B = cu.size[0] - 1;
+    if (B < 0 || !fits32(B, "num_requests")) {
+        if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "cu_beams must have num_requests + 1 entries");
+        return nullptr;
+    }
+    if (!load(a[0], "scores_out", &dev, &so)) return nullptr;
+    if (so.dim != 2) {
+        PyErr_SetString(PyExc_ValueError, "scores_out must be [num_requests, num_select]");
+        return nullptr;
+    }
+    const int64_t K = so.size[1];
+    if (!fits32(K, "num_select") || !exact(a[0], "scores_out", &dev, t_f32, B, K, &so) ||
+        !exact(a[1], "rows_out", &dev, t_i32, B, K, &ro) || !exact(a[2], "tokens_out", &dev, t_i32, B, K, &to) ||
+        !exact(a[4], "scores", &dev, t_f32, R, -1, &scores) ||
+        (a[6] != Py_None && !exact(a[6], "allowed", &dev, t_i32, R, words, &allowed)) || !as_int(a[8], &end_token) ||
+        !workspace_of(a[9], &dev, &ws, &ws_bytes) || !status_of(a[10], &dev, &status))
+        return nullptr;
+    if (a[7] != Py_None) {
+        if (!load(a[7], "ended", &dev, &ended)) return nullptr;
+        if (ended.dtype != t_u8 && ended.dtype != t_bool) {
+            PyErr_SetString(PyExc_TypeError, "ended must be uint8 or bool");
+            return nullptr;
+        }
+        if (ended.dim != 1 || ended.size[0] != R) {
+            PyErr_SetString(PyExc_ValueError, "ended must have an entry for each row");
+            return nullptr;
+        }
+    }
+    return on_device(dev, [&](pa_stream_t s) {
+        return c_select(static_cast<float*>(so.ptr), static_cast<int32_t*>(ro.ptr), static_cast<int32_t*>(to.ptr), x.ptr, dt,
+                        R > 1 ? stride[0] : V, static_cast<int32_t>(V), static_cast<int32_t>(R),
+                        static_cast<const float*>(scores.ptr), static_cast<const int32_t*>(cu.ptr), static_cast<int32_t>(B),
+                        static_cast<const uint32_t*>(allowed.ptr), words, static_cast<const uint8_t*>(ended.ptr),
+                        static_cast<int32_t>(end_token), static_cast<int32_t>(K), ws, static_cast<size_t>(ws_bytes), status,
+                        s);
+    });
+}
+
+// (address of the layers' pa_kv_cache array, their number, the first layer's k_cache, parents, block_table, seq_lens,
+// spare_blocks, block_table_out, seq_lens_out, slot_mapping_out, spare_used_out, dev_status)
+PyObject* beam_reorder(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    int64_t dev = -1, layers;
+    Tensor k, parents, table, lens, spare, t2, l2, slots, used;
+    int32_t* status;
+    if (!count(n, 12)) return nullptr;
+    const auto* caches = static_cast<const pa_kv_cache*>(PyLong_AsVoidPtr(a[0]));
+    if (caches == nullptr) {
+        if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "no layers");
+        return nullptr;
+    }
+    if (!as_int(a[1], &layers) || !load(a[2], "k_cache", &dev, &k) ||
+        !exact(a[3], "parents", &dev, t_i32, -2, -1, &parents) || !load(a[4], "block_table", &dev, &table))
+        return nullptr;
+    if (table.dim != 2 || table.dtype != t_i32) {
+        PyErr_SetString(table.dim != 2 ? PyExc_ValueError : PyExc_TypeError, "block_table must be int32 [rows, max_blocks]");
+        return nullptr;
+    }
+    const int64_t m = parents.size[0], rows = table.size[0], width = table.size[1];
+    if (!fits32(m, "num_rows") || !fits32(rows, "num_rows_in") || !fits32(width, "max_blocks") ||
+        !exact(a[5], "seq_lens", &dev, t_i32, rows, -1, &lens) || !exact(a[6], "spare_blocks", &dev, t_i32, m, -1, &spare) ||
+        !exact(a[7], "block_table_out", &dev, t_i32, m, width, &t2) || !exact(a[8], "seq_lens_out", &dev, t_i32, m, -1, &l2) ||
+        !exact(a[9], "slot_mapping_out", &dev, t_i64, m, -1, &slots) ||
+        !exact(a[10], "spare_used_out", &dev, t_i32, m, -1, &used) || !status_of(a[11], &dev, &status))
+        return nullptr;
+    return on_device(dev, [&](pa_stream_t s) {
+        return c_reorder(caches, static_cast<int32_t>(layers), static_cast<const int32_t*>(parents.ptr),
+                         static_cast<int32_t>(m), static_cast<const int32_t*>(table.ptr), static_cast<int32_t>(rows),
+                         static_cast<int32_t>(width), static_cast<const int32_t*>(lens.ptr),
+                         static_cast<const int32_t*>(spare.ptr), static_cast<int32_t*>(t2.ptr), static_cast<int32_t*>(l2.ptr),
+                         static_cast<int64_t*>(slots.ptr), static_cast<int32_t*>(used.ptr), status, s);
+    });
+}
+
+// setup_beams(uint8, bool; addresses of pa_varlen_cascade, pa_beam_select, pa_beam_reorder), after setup()
+PyObject* setup_beams(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (!count(n, 5)) return nullptr;
+    void* f[3];
+    for (int i = 0; i < 3; ++i) {
+        f[i] = PyLong_AsVoidPtr(a[2 + i]);
+        if (f[i] == nullptr) {
+            if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "a function's address is missing");
+            return nullptr;
+        }
+    }
+    t_u8 = Py_NewRef(a[0]);
+    t_bool = Py_NewRef(a[1]);
+    c_cascade = reinterpret_cast<decltype(c_cascade)>(f[0]);
+    c_select = reinterpret_cast<decltype(c_select)>(f[1]);
+    c_reorder = reinterpret_cast<decltype(c_reorder)>(f[2]);
+    Py_RETURN_NONE;
+}
+
 // setup(dtypes: float16, bfloat16, float8_e4m3fn, int32, int64, float32; get_device, set_device, get_stream;
 // addresses of pa_qk_norm_rope, pa_qk_norm_rope_write, pa_decode_window, pa_prefill_varlen_window)
 PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -422,12 +614,25 @@ PyObject* ready(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     return F(self, a, n);
 }
 
+template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
+PyObject* beams_ready(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    if (c_rope == nullptr || c_cascade == nullptr) {
+        PyErr_SetString(PyExc_RuntimeError, "setup() and setup_beams() have not been called");
+        return nullptr;
+    }
+    return F(self, a, n);
+}
+
 #define PA_METHOD(NAME, F) {NAME, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {PA_METHOD("setup", setup),
                          PA_METHOD("qk_norm_rope", ready<qk_norm_rope>),
                          PA_METHOD("qk_norm_rope_write", ready<qk_norm_rope_write>),
                          PA_METHOD("decode_window", ready<decode_window>),
                          PA_METHOD("prefill_varlen_window", ready<prefill_varlen_window>),
+                         PA_METHOD("setup_beams", setup_beams),
+                         PA_METHOD("varlen_cascade", beams_ready<varlen_cascade>),
+                         PA_METHOD("beam_select", beams_ready<beam_select>),
+                         PA_METHOD("beam_reorder", beams_ready<beam_reorder>),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
