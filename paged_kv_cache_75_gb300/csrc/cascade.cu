@@ -52,6 +52,32 @@ constexpr int kSmemBytes = kOffItems + kItemCache * 32;
 static_assert(kOffMisc % 8 == 0 && kOffPend % 8 == 0 && kOffItems % 8 == 0 && kSmemBytes % 4 == 0, "alignment");
 constexpr int kMaxSegments = 6144;  // num_seqs + num_groups (the prefix array in shared memory)
 
+// A K or V tile in shared memory: groups of eight keys, 2 KB each, of which the first 1 KB
+// holds the columns 0 .. 63 (128-byte rows, swizzled) and the second 64 .. 127.  So a whole
+// page is one box of a 4-D view of the cache, {64 columns, 8 keys, 2 halves, groups}: with a
+// box for each half, a tile's TMA instructions (32 at block size 16) bounded the loads.
+constexpr int kGroupBytes = 2048;
+__device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap* map, int group, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3}], "
+        "[%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(group), "r"(bar)
+        : "memory");
+}
+inline bool make_page_map(CUtensorMap* map, const void* base, int64_t rows, int dtype, int block_size) {
+    auto fn = encode_fn();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[4] = {64, 8, 2, static_cast<cuuint64_t>(rows / 8)};
+    const cuuint64_t strides[3] = {kD * 2, 128, 8 * kD * 2};
+    const cuuint32_t box[4] = {64, 8, 2, static_cast<cuuint32_t>(block_size / 8)};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    const CUresult r = fn(map, dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                          4, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 struct CascadeParams {
     void* out;
     const uint16_t* q;  // NULL (test hook): no copy is issued, every wait runs out
@@ -81,6 +107,11 @@ struct CascadeParams {
     int32_t max_parts;
     int32_t own;        // the sequences' own keys too, or the prefixes alone
     int32_t stack;      // groups share; 0: every sequence's keys are one segment
+    // own = 0: the own keys' parts, written by the decode kernel, are of own_part keys and
+    // numbered from own_base; it takes the sequences' lengths from ws_lens
+    int32_t own_base;
+    int32_t own_part;
+    int32_t* ws_lens;
     int32_t order_cap;  // entries the shared-memory work order holds (set by the launch)
     float scale_log2;   // scale * log2(e)
 };
@@ -388,6 +419,18 @@ cascade_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
         build_order(p, prefix, n_seg, n_entries, ord, ord + p.order_cap);
         order = ord;
     }
+    // what the decode kernel goes by: a sequence's length, or its shared length where it
+    // has no query (no keys of its own)
+    if (!p.own && blockIdx.x == 0) {
+        for (int b = tid; b < p.num_seqs; b += kThreads) {
+            int q0, lq, lk;
+            const bool ok = seq_lens_ok(p, b, q0, lq, lk);
+            const Group g = group_of_seq(p, b);
+            const bool good = ok && g.ok && (lq == 0 || (g.s0 <= lk - lq && q0 == b));
+            if (!good) report(p.status, PA_ERR_INVALID_ARG);
+            p.ws_lens[b] = good && lq == 1 ? lk : g.ok ? g.s0 : 0;
+        }
+    }
     const uint32_t tmem = uniform(*tmem_slot);
     const int n_items = n_entries * p.num_kv_heads;
     // this CTA's first kItemCache items, worked out once: every role's item
@@ -422,32 +465,32 @@ cascade_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
             for (int rnd = 0, item; ok && (item = snake_item(rnd, n_items)) >= 0; ++rnd) {
                 const Work w = item_work(rnd, item);
                 const int32_t* bt_row = p.block_table + static_cast<int64_t>(w.tab) * p.max_blocks + w.entry0;
-                // page ids come in batches of 32 (one per lane, -1: past Lk, -2:
-                // bad id), so the table's latency is paid once per batch
+                // Page ids come in batches of four tiles (a lane each, -1: past the keys,
+                // -2: bad id), the next batch's ahead of time
                 const int ntiles = w.tiles();
                 const int pages = (w.nkeys + p.block_size - 1) / p.block_size;
-                int32_t id = -1;
+                auto ids_from = [&](int pg0) -> int32_t {
+                    const int pg = pg0 + lane;
+                    if (lane >= 4 * ppt || pg >= pages) return -1;
+                    const int32_t x = __ldg(bt_row + pg);
+                    if (x >= 0 && x < p.num_blocks) return x;
+                    // both loader warps read the id; one reports it
+                    if (kv == 0) report(p.status, PA_ERR_BAD_BLOCK);
+                    return -2;
+                };
+                int32_t id = -1, id_next = ntiles > 0 ? ids_from(0) : -1;
                 for (int t = 0; t < ntiles && ok; ++t) {
-                    const int pg0 = t * ppt;  // first page of this tile
-                    if ((pg0 & 31) == 0) {
-                        const int pg = pg0 + lane;
-                        id = -1;
-                        if (pg < pages) {
-                            id = __ldg(bt_row + pg);
-                            if (id < 0 || id >= p.num_blocks) {
-                                // both loader warps read the id; one reports it
-                                if (kv == 0) report(p.status, PA_ERR_BAD_BLOCK);
-                                id = -2;
-                            }
-                        }
+                    if ((t & 3) == 0) {
+                        id = id_next;
+                        id_next = t + 4 < ntiles ? ids_from((t + 4) * ppt) : -1;
                     }
                     // lane k < ppt holds the id of page k of this tile
-                    const int my_id = __shfl_sync(0xffffffffu, id, (pg0 + (lane & 7)) & 31);
+                    const int from = (t & 3) * ppt + (lane & 7);
+                    const int my_id = __shfl_sync(0xffffffffu, id, from & 31);
                     const bool have = lane < ppt && my_id >= 0;
                     const uint32_t bytes =
                         static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, have))) * 2u * p.block_size * kD;
-                    const int row = (my_id * p.num_kv_heads + w.kvh) * p.block_size;
-                    const uint32_t off = lane * p.block_size * 128;  // page lane's rows in a 64-column block
+                    const int group = (my_id * p.num_kv_heads + w.kvh) * (p.block_size / 8);
                     const uint32_t full = full0 + 8 * stage;
                     if (lane == 0) ok = mbar_wait(empty0 + 8 * stage, phase ^ 1u, p.status, abort_flag);
                     ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -457,11 +500,7 @@ cascade_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                         else mbar_arrive(full);
                     }
                     __syncwarp();
-                    if (have) {
-                        const uint32_t dst = ring + stage * kTileBytes + off;
-                        tma_load_2d(dst, map, 0, row, full);
-                        tma_load_2d(dst + kBlkBytes, map, 64, row, full);
-                    }
+                    if (have) tma_load_page(ring + stage * kTileBytes + lane * p.block_size * (kD * 2), map, group, full);
                     ++fill;
                     if (++stage == nst) {
                         stage = 0;
@@ -555,8 +594,8 @@ cascade_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
         const uint32_t id_pv = mma_idesc(DT == PA_BF16 ? 1 : 0, kRows, kD, 1);
         // descriptors are built once; a k-step only adds a constant to the
         // start-address field (bits 0..13, in 16-byte units)
-        const uint64_t dk = smem_desc(smem_addr(sK), 16, 1024);
-        const uint64_t dv = smem_desc(smem_addr(sV), kBlkBytes, 1024);
+        const uint64_t dk = smem_desc(smem_addr(sK), 16, kGroupBytes);
+        const uint64_t dv = smem_desc(smem_addr(sV), kGroupBytes / 2, kGroupBytes);
         const uint64_t dq = smem_desc(smem_addr(sQ), 16, 1024);
         if (elect_one()) {
             uint32_t k_stage = 0, k_phase = 0;  // K ring position of the next QK
@@ -572,9 +611,9 @@ cascade_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                 const uint64_t dks = dk + k_stage * (kTileBytes >> 4);
 #pragma unroll
                 for (int k = 0; k < kD / 16; ++k) {
-                    // Q and K: 32 bytes per k-step in a 64-column block
-                    const uint32_t step = (k / 4) * (kBlkBytes >> 4) + (k % 4) * 2;
-                    mma_f16_ss(tmem + kColS + b * kBN, dq + step, dks + step, id_qk, k > 0 ? 1u : 0u);
+                    // Q and K: 32 bytes per k-step in a 64-column half
+                    mma_f16_ss(tmem + kColS + b * kBN, dq + (k / 4) * (kBlkBytes >> 4) + (k % 4) * 2,
+                               dks + (k / 4) * (kGroupBytes >> 5) + (k % 4) * 2, id_qk, k > 0 ? 1u : 0u);
                 }
                 mma_commit(s_full + 8 * b);
                 mma_commit(k_empty + 8 * k_stage);
@@ -621,9 +660,9 @@ cascade_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
 #pragma unroll
                         for (int j = 0; j < kBN / 16; ++j) {
                             // keys 16j..16j+15: P at 8 columns of half j/4 (hi at +0, lo at +32);
-                            // V: 2048 bytes per 16 keys
+                            // V: two groups per 16 keys
                             mma_f16_ts(col_o, tmem + kColS + y * kBN + (j / 4) * 64 + part * 32 + (j % 4) * 8,
-                                       dvs + j * (2048 >> 4), id_pv, (t > 0 || part > 0 || j > 0) ? 1u : 0u);
+                                       dvs + j * (2 * kGroupBytes >> 4), id_pv, (t > 0 || part > 0 || j > 0) ? 1u : 0u);
                         }
                     }
                     mma_commit(v_empty + 8 * v_stage);
@@ -930,7 +969,7 @@ cascade_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                     const int rest = w.nkeys - t * kBN;
                     for (int ci = u; ci < (kBN - rest) * 16; ci += 256) {
                         const int rr = rest + (ci >> 4), c = ci & 15;
-                        *reinterpret_cast<uint4*>(vt + (c >> 3) * kBlkBytes + sw128(rr, c & 7)) =
+                        *reinterpret_cast<uint4*>(vt + (rr >> 3) * kGroupBytes + (c >> 3) * (kGroupBytes / 2) + sw128(rr & 7, c & 7)) =
                             make_uint4(0u, 0u, 0u, 0u);
                     }
                     fence_async_smem();
@@ -990,15 +1029,17 @@ __global__ void __launch_bounds__(256) cascade_merge_kernel(const CascadeParams 
     const Group g = group_of_seq(p, b);
     if (!g.ok || g.s0 > lk - lq) return;
     const int start = g.shares ? g.s0 : 0;
-    if (start == 0 && lk <= p.part) return;  // one part, already in out
+    if (p.own && start == 0 && lk <= p.part) return;  // one part, already in out
     const int i = static_cast<int>(pair / p.num_heads);
     const int seen = lk - lq + i + 1 - start;  // own keys
-    const int np = (start > 0 ? ceil_div(start, p.part) : 0) + (seen > 0 ? ceil_div(seen, p.part) : 0);
+    const int pre = start > 0 ? ceil_div(start, p.part) : 0;
+    const int np = pre + (seen > 0 ? ceil_div(seen, p.own ? p.part : p.own_part) : 0);
+    const int skip = p.own ? 0 : p.own_base - pre;  // numbers between the prefix's parts and the own keys'
     const int64_t row = static_cast<int64_t>(q0) * p.num_heads + pair;
     const float* lse = p.ws_lse + row * p.max_parts;
     const float4* o = reinterpret_cast<const float4*>(p.ws_o + row * p.max_parts * kD) + lane;
     float M = -INFINITY;
-    for (int j = lane; j < np; j += 32) M = fmaxf(M, lse[j]);
+    for (int j = lane; j < np; j += 32) M = fmaxf(M, lse[j < pre ? j : j + skip]);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1006,8 +1047,9 @@ __global__ void __launch_bounds__(256) cascade_merge_kernel(const CascadeParams 
     if (M > -INFINITY) {
 #pragma unroll 4
         for (int j = 0; j < np; ++j) {
-            const float w = ex2(lse[j] - M);
-            const float4 v = o[static_cast<int64_t>(j) * (kD / 4)];
+            const int at = j < pre ? j : j + skip;
+            const float w = ex2(lse[at] - M);
+            const float4 v = o[static_cast<int64_t>(at) * (kD / 4)];
             sum += w;
             acc.x = fmaf(w, v.x, acc.x);
             acc.y = fmaf(w, v.y, acc.y);
@@ -1024,10 +1066,11 @@ __global__ void __launch_bounds__(256) cascade_merge_kernel(const CascadeParams 
 constexpr int kSms = 152;
 
 struct Plan {
-    bool stack;
-    int part, max_parts;
-    size_t o_off, bytes;
+    bool stack, own;
+    int part, max_parts, own_base;
+    size_t o_off, lens_off, bytes;
 };
+constexpr int kOwnPart = 1024;  // the decode kernel's parts
 
 // How the batch is cut, from what the host knows of it.
 //
@@ -1037,10 +1080,15 @@ struct Plan {
 // 16 to 1024 tokens behind them, 32/8 heads, bf16: PLAN_PROMPTS_STACKED us stacked, PLAN_PROMPTS
 // not.)  With few query tiles over long keys they are cut into parts all the same.
 //
+// Own keys of one-token sequences.  A tile of 128 rows for one query token's heads pays its
+// start and end (some 5 us, few of them hidden) for a handful of keys: past one round of
+// items they go to the decode kernel, which takes the same slots.  (32 requests of eight beams,
+// up to 256 tokens of their own: OWN_TILES us in tiles, OWN_DECODE by the decode kernel.)
+//
 // Parts.  n parts of the longest prefix make tiles * n items for the SMs' rounds; an item
 // costs its key tiles and some 2.5 more for its start and end, a part's rows 1 KB of traffic
 // a row and head.  The n with the least such time is taken.
-Plan plan_of(int64_t num_seqs, int64_t total_q, int num_heads, int num_kv_heads, int max_k, int max_shared) {
+Plan plan_of(int64_t num_seqs, int64_t total_q, int num_heads, int num_kv_heads, int max_q, int max_k, int max_shared) {
     Plan r;
     const int group = num_heads / num_kv_heads;
     const int64_t tiles = (total_q * group + kRows - 1) / kRows * num_kv_heads;
@@ -1061,20 +1109,23 @@ Plan plan_of(int64_t num_seqs, int64_t total_q, int num_heads, int num_kv_heads,
         }
         if (part == 2 * kBN) break;
     }
+    r.own = !(r.stack && max_q == 1 && total_q >= num_seqs && (tiles + num_seqs * num_kv_heads) > kSms);
+    r.own_base = (max_shared + r.part - 1) / r.part;
     // (not stacked and one part: everything goes straight to out)
-    r.max_parts = !r.stack && max_k <= r.part ? 1 : (max_k + r.part - 1) / r.part + 1;
-    if (r.max_parts == 1) {
-        r.o_off = r.bytes = 0;
-        return r;
-    }
+    r.max_parts = !r.own                          ? r.own_base + (max_k + kOwnPart - 1) / kOwnPart
+                  : !r.stack && max_k <= r.part ? 1
+                                                  : (max_k + r.part - 1) / r.part + 1;
+    r.o_off = r.lens_off = r.bytes = 0;
+    if (r.max_parts == 1) return r;
     const size_t rows = static_cast<size_t>(total_q) * num_heads * r.max_parts;
     r.o_off = (rows * 4 + 255) & ~static_cast<size_t>(255);
-    r.bytes = r.o_off + rows * kD * 4 + 16;  // (32-byte stores: the pointer is rounded up)
+    r.lens_off = r.o_off + rows * kD * 4;
+    r.bytes = r.lens_off + (r.own ? 0 : static_cast<size_t>(num_seqs) * 4) + 16;  // (32-byte stores: the pointer is rounded up)
     return r;
 }
 
 template <int DT>
-pa_status launch_cascade(CascadeParams p, const CUtensorMap& map_k, const CUtensorMap& map_v, const CUtensorMap& map_q,
+pa_status launch_cascade(CascadeParams p, const pa_kv_cache& cache, const CUtensorMap& map_k, const CUtensorMap& map_v, const CUtensorMap& map_q,
                          cudaStream_t stream) {
     const int n_seg = p.num_groups + (p.own ? p.num_seqs : 0);
     const int base = kSmemBytes + (n_seg + 1) * 4 + 1024;
@@ -1086,15 +1137,46 @@ pa_status launch_cascade(CascadeParams p, const CUtensorMap& map_k, const CUtens
     const int64_t room = (device_max_smem_optin() - 2048 - base) / 4 - (kThreads / 32) * 64;
     p.order_cap = static_cast<int32_t>(room <= 0 ? 0 : (bound < room ? bound : room));
     const int smem = base + (p.order_cap > 0 ? (p.order_cap + (kThreads / 32) * 64) * 4 : 0);
-    static LaunchCache cache;
+    static LaunchCache launch_cache;
     auto kern = cascade_kernel<DT>;
-    const int per_sm = blocks_per_sm(kern, kThreads, smem, cache);
+    const int per_sm = blocks_per_sm(kern, kThreads, smem, launch_cache);
     if (per_sm <= 0) return PA_ERR_CUDA;
     const int64_t max_items = bound * p.num_kv_heads;
     const int64_t cap = static_cast<int64_t>(device_sm_count()) * per_sm;
     const int grid = static_cast<int>(max_items < cap ? max_items : cap);
     if (grid > 0 && launch_pdl(kern, grid, kThreads, smem, stream, map_k, map_v, map_q, p) != cudaSuccess) return PA_ERR_CUDA;
     if (p.max_parts == 1) return PA_OK;
+    if (!p.own) {
+        DecodeParams d{};
+        d.q = p.q;
+        d.k_cache = static_cast<const uint8_t*>(cache.k_cache);
+        d.v_cache = static_cast<const uint8_t*>(cache.v_cache);
+        d.block_table = p.block_table;
+        d.seq_lens = p.ws_lens;
+        d.ws_lse = p.ws_lse;
+        d.ws_o = p.ws_o;
+        d.status = p.status;
+        d.num_blocks = p.num_blocks;
+        d.block_size = p.block_size;
+        d.num_kv_heads = p.num_kv_heads;
+        d.num_heads = p.num_heads;
+        d.num_seqs = d.num_members = p.num_seqs;
+        d.max_blocks = p.max_blocks;
+        d.max_seq_len = p.max_k;
+        d.partition = p.own_part;
+        d.max_parts = p.max_parts;
+        d.qk_scale = p.scale_log2;
+        d.v_scale = d.k_scale_w = d.v_scale_w = 1.f;
+        d.cu_groups = p.cu_groups;
+        d.shared_lens = p.shared_lens;
+        d.num_groups = p.num_groups;
+        d.own_base = p.own_base;
+        pa_status (*const launch[2][3])(const DecodeParams&, int, int, int, cudaStream_t) = {
+            {launch_decode_f16_bs16, launch_decode_f16_bs32, launch_decode_f16_bs64},
+            {launch_decode_bf16_bs16, launch_decode_bf16_bs32, launch_decode_bf16_bs64}};
+        const pa_status st = launch[DT == PA_BF16][p.block_size == 16 ? 0 : p.block_size == 32 ? 1 : 2](d, DT, kD, p.group, stream);
+        if (st != PA_OK) return st;
+    }
     const int64_t per_seq = (static_cast<int64_t>(p.max_q) * p.num_heads + 7) / 8;
     if (per_seq > INT32_MAX) return PA_ERR_UNSUPPORTED;
     const dim3 mgrid(static_cast<unsigned>(per_seq), static_cast<unsigned>(p.num_seqs));
@@ -1112,7 +1194,7 @@ extern "C" size_t pa_varlen_cascade_workspace_size(int32_t num_seqs, int64_t tot
     if (num_seqs <= 0 || total_q <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads != 0 ||
         head_size <= 0 || max_seqlen_q <= 0 || max_seqlen_k < 0 || max_shared_len < 0 || block_size <= 0)
         return 0;
-    return plan_of(num_seqs, total_q, num_heads, num_kv_heads, max_seqlen_k, max_shared_len).bytes;
+    return plan_of(num_seqs, total_q, num_heads, num_kv_heads, max_seqlen_q, max_seqlen_k, max_shared_len).bytes;
 }
 
 extern "C" pa_status pa_varlen_cascade(void* out, const void* q, pa_dtype q_dtype, const pa_kv_cache* cache,
@@ -1147,7 +1229,7 @@ extern "C" pa_status pa_varlen_cascade(void* out, const void* q, pa_dtype q_dtyp
     if (static_cast<int64_t>(num_seqs) + num_groups > kMaxSegments) return PA_ERR_UNSUPPORTED;
     const int64_t rows = cache->num_blocks * cache->num_kv_heads * bs;
     if (rows > INT32_MAX || total_q > INT32_MAX - kRows) return PA_ERR_UNSUPPORTED;
-    const Plan plan = plan_of(num_seqs, total_q, num_heads, cache->num_kv_heads, max_seqlen_k, max_shared_len);
+    const Plan plan = plan_of(num_seqs, total_q, num_heads, cache->num_kv_heads, max_seqlen_q, max_seqlen_k, max_shared_len);
     if (plan.bytes > 0 && (workspace == nullptr || workspace_bytes < plan.bytes || (reinterpret_cast<uintptr_t>(workspace) & 15u)))
         return PA_ERR_INVALID_ARG;
 
@@ -1179,15 +1261,18 @@ extern "C" pa_status pa_varlen_cascade(void* out, const void* q, pa_dtype q_dtyp
     p.total_q = static_cast<int32_t>(total_q);
     p.part = plan.part;
     p.max_parts = plan.max_parts;
-    p.own = 1;
+    p.own = plan.own ? 1 : 0;
+    p.own_base = plan.own_base;
+    p.own_part = kOwnPart;
+    p.ws_lens = reinterpret_cast<int32_t*>(ws + plan.lens_off);
     p.stack = plan.stack ? 1 : 0;
     p.scale_log2 = scale * 1.4426950408889634f;
     CUtensorMap map_k, map_v, map_q;
-    if (!make_cache_map(&map_k, cache->k_cache, rows, q_dtype, bs) ||
-        !make_cache_map(&map_v, cache->v_cache, rows, q_dtype, bs) ||
+    if (!make_page_map(&map_k, cache->k_cache, rows, q_dtype, bs) ||
+        !make_page_map(&map_v, cache->v_cache, rows, q_dtype, bs) ||
         !make_q_map(&map_q, q, num_heads, group, p.total_q, q_dtype))
         return PA_ERR_CUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return q_dtype == PA_BF16 ? launch_cascade<PA_BF16>(p, map_k, map_v, map_q, s)
-                              : launch_cascade<PA_F16>(p, map_k, map_v, map_q, s);
+    return q_dtype == PA_BF16 ? launch_cascade<PA_BF16>(p, *cache, map_k, map_v, map_q, s)
+                              : launch_cascade<PA_F16>(p, *cache, map_k, map_v, map_q, s);
 }

@@ -82,6 +82,9 @@ struct DecodeParams {
     const int32_t* cu_groups;
     const int32_t* shared_lens;
     int32_t num_groups;
+    // suffix pass of pa_varlen_cascade (> 0): its partials' first number, whatever the
+    // prefix pass's parts, and no merge launch (the caller has its own)
+    int32_t own_base;
     // cascade decode in one launch ("group mode", vm > 0).  Sequence b <
     // vcount of the launch is the members cu_groups[g] + j*vm .. + vm-1 (those
     // that exist) of group g = b / vpg, j = b % vpg, over the group's first
@@ -200,6 +203,7 @@ __device__ __forceinline__ int parts_of(int L, int P) { return L <= P ? 1 : (L +
 
 // cascade: workspace parts the prefix pass filled for a shared length s0
 __device__ __forceinline__ int prefix_parts(const DecodeParams& p, int s0) {
+    if (p.own_base > 0) return p.own_base;
     return p.cu_groups != nullptr ? (s0 + p.partition - 1) / p.partition : 0;
 }
 

@@ -46,7 +46,7 @@ pa_status launch_decode_t(DecodeParams p, cudaStream_t stream) {
     if (grid <= 0) return PA_OK;
     p.one_round = mode == kWindow && max_items <= cap ? 1 : 0;
     if (launch_pdl(kern, grid, C::THREADS, smem, stream, p) != cudaSuccess) return PA_ERR_CUDA;
-    if (p.max_parts > 1) {
+    if (p.max_parts > 1 && p.own_base == 0) {
         // group mode: the merge runs over the batch's members
         DecodeParams r = p;
         if (r.vm > 0) {

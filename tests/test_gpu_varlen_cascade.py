@@ -200,3 +200,70 @@ def test_binding_refusals():
                   (dict(max_shared_len=65), pk.PaError), (dict(scale=-1.0), pk.PaError)):
         with pytest.raises(e):
             pk.pa_varlen_cascade(**a(**kw))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("heads,kv_heads,bs", [(8, 8, 16), (16, 8, 32), (32, 8, 64), (64, 8, 16)])
+def test_decode_batches(dtype, heads, kv_heads, bs):
+    """One token a sequence, enough of them that the decode kernel takes their own keys: groups of many, of one, without
+    a prefix, own keys of one token and of more than one part."""
+    groups = [(20 * bs, own(15, 1, 300)), (bs, own(1, 2, 40)), (0, own(3, 3, 200)), (2048, [(2500, 1), (1, 1), (1024, 1), (1025, 1)]),
+              (7 * bs, own(2, 4, 5))]
+    b = Batch(groups, heads, kv_heads, dtype, bs, 21, pad_rows=4).device()
+    b.check(b.run())
+    b.check(b.run(max_k=9000, max_shared=4096, max_group=99))
+
+
+def test_padded_decode_batch():
+    """Sequences without a query behind the others (their rows too are left as they were)."""
+    b = Batch([(320, own(20, 5, 90)), (64, own(2, 6, 9)), (0, [(0, 0)] * 4)], 32, 8, "bf16", 16, 22, pad_rows=4).device()
+    b.check(b.run())
+
+
+def test_decode_batch_with_a_gap():
+    """Sequences without a query between the others: by tiles where q has a row a query, else reported."""
+    groups = [(320, [(9, 1), (5, 0), (40, 1)] * 8)]
+    b = Batch(groups, 32, 8, "bf16", 16, 23).device()
+    b.check(b.run())
+    b = Batch(groups, 32, 8, "bf16", 16, 23, pad_rows=8).device()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    b.run(status)
+    assert int(status) == 1
+
+
+@pytest.mark.parametrize("what", ["late", "partial", "row", "block", "max_k"])
+def test_decode_reported(what):
+    b = Batch([(64, own(20, 1, 50)), (96, own(3, 2, 40))], 32, 8, "bf16", 16, 24).device()
+    more, code = {}, 1
+    if what == "late":
+        b.sh[1] = 192
+        more = dict(max_shared=192, max_k=300)
+    elif what == "partial":
+        b.sh[1] = 90
+    elif what == "row":
+        b.tab[22, 2] = b.tab[0, 0]
+    elif what == "block":
+        b.tab[20:, 1], code = b.kc.shape[0], 6
+    else:
+        more = dict(max_k=int(b.lk[20:].max()) - 1)
+        assert int(b.lk[:20].max()) <= more["max_k"]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = b.run(status, **more)
+    assert int(status) == code
+    b.tab = torch.from_numpy(b.table).cuda()
+    b.check(out, torch.arange(20, device="cuda"))
+
+
+def test_decode_captured():
+    b = Batch([(640, own(30, 1, 90))], 32, 8, "bf16", 16, 25).device()
+    want = b.run()
+    out, ws, st = torch.empty_like(b.qd), b.workspace(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    b.call(out, ws, st)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        b.call(out, ws, st)
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
