@@ -104,12 +104,15 @@ struct CascadeParams {
     int32_t max_shared;
     int32_t total_q;
     int32_t part;       // keys of a part (a multiple of kBN)
+    int32_t tail_from;  // a prefix's query tiles from this one on
+    int32_t tail_part;  // have parts of so many keys instead
     int32_t max_parts;
     int32_t own;        // the sequences' own keys too, or the prefixes alone
     int32_t stack;      // groups share; 0: every sequence's keys are one segment
-    // own = 0: the own keys' parts, written by the decode kernel, are of own_part keys and
-    // numbered from own_base; it takes the sequences' lengths from ws_lens
-    int32_t own_base;
+    int32_t own_base;   // behind a prefix, the own keys' parts are numbered from here
+    // own = 0: these parts, of own_part keys, are the decode kernel's, which takes the
+    // sequences' lengths from ws_lens
+
     int32_t own_part;
     int32_t* ws_lens;
     int32_t order_cap;  // entries the shared-memory work order holds (set by the launch)
@@ -165,7 +168,8 @@ struct Segment {
     int q0, nq;       // its query rows
     int start, len;   // its keys: positions start .. start + len - 1
     int shift;        // query row i sees the first shift + i + 1 of them
-    int tiles, parts;
+    int tiles, parts; // (of a prefix's tiles from tail_from on: tail_parts)
+    int tail_parts;
     int part0;        // its first part's number, -1: its rows have this part alone
 };
 constexpr int kNoMask = 1 << 30;
@@ -185,6 +189,7 @@ __device__ __forceinline__ Segment segment(const CascadeParams& p, int s, bool c
         r.shift = kNoMask;
         r.tiles = ceil_div(r.nq, p.tq);
         r.parts = ceil_div(g.s0, p.part);
+        r.tail_parts = ceil_div(g.s0, p.tail_part);
         return r;
     }
     const int b = s - p.num_groups;
@@ -202,8 +207,14 @@ __device__ __forceinline__ Segment segment(const CascadeParams& p, int s, bool c
     r.shift = r.len - lq;
     r.tiles = ceil_div(lq, p.tq);
     r.parts = r.len <= p.part ? 1 : ceil_div(r.len, p.part);
-    r.part0 = r.start > 0 ? ceil_div(r.start, p.part) : r.parts > 1 ? 0 : -1;
+    r.part0 = r.start > 0 ? p.own_base : r.parts > 1 ? 0 : -1;
     return r;
+}
+
+// entries of a segment
+__device__ __forceinline__ int entries(const CascadeParams& p, const Segment& g) {
+    const int tail = g.shift == kNoMask ? max(0, g.tiles - p.tail_from) : 0;
+    return (g.tiles - tail) * g.parts + tail * g.tail_parts;
 }
 
 struct Work {
@@ -225,17 +236,24 @@ __device__ __forceinline__ Work entry_work(const CascadeParams& p, const int32_t
         else hi = mid - 1;
     }
     const Segment g = segment(p, lo, false);
-    const int e = entry - prefix[lo], parts = max(g.parts, 1);
-    const int tile = e / parts, part = e - tile * parts;
+    int e = entry - prefix[lo], tile = 0, parts = max(g.parts, 1), size = p.part;
+    if (g.shift == kNoMask && e >= p.tail_from * static_cast<int64_t>(parts)) {
+        e -= p.tail_from * parts;
+        tile = p.tail_from;
+        parts = max(g.tail_parts, 1);
+        size = p.tail_part;
+    }
+    const int part = e % parts;
+    tile += e / parts;
     Work w;
-    const int i0 = tile * p.tq, k0 = part * p.part;
+    const int i0 = tile * p.tq, k0 = part * size;
     w.tab = g.tab;
     w.entry0 = (g.start + k0) / p.block_size;
     w.tok0 = g.q0 + i0;
     w.ntok = min(p.tq, g.nq - i0);
     w.kvh = 0;
     w.shift = g.shift == kNoMask ? kNoMask : g.shift + i0 - k0;
-    w.nkeys = min(min(p.part, g.len - k0), w.shift + w.ntok);
+    w.nkeys = min(min(size, g.len - k0), w.shift + w.ntok);
     w.part = g.part0 < 0 ? -1 : g.part0 + part;
     return w;
 }
@@ -255,7 +273,7 @@ __device__ __forceinline__ Work work_item(const CascadeParams& p, const int32_t*
 // turns the [warp][class] counts into class-major offsets, each warp then places its
 // chunk in order.  All threads of the block take part; hist holds 12*64 ints.
 __device__ __forceinline__ int entry_class(const CascadeParams& p, const int32_t* prefix, int n_seg, int entry) {
-    const int most = p.part / kBN;
+    const int most = max(p.part, p.tail_part) / kBN;
     const int n = min(most, entry_work(p, prefix, n_seg, entry).tiles());
     return 63 - static_cast<int>((static_cast<int64_t>(n) * 64) / (most + 1));  // 0 = most key tiles
 }
@@ -393,7 +411,7 @@ cascade_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
         for (int s = s0; s < s1; ++s) {
             const Segment g = segment(p, s, true);
             prefix[s] = local;
-            local += g.tiles * g.parts;
+            local += entries(p, g);
         }
         int v = local;
 #pragma unroll
@@ -1032,9 +1050,11 @@ __global__ void __launch_bounds__(256) cascade_merge_kernel(const CascadeParams 
     if (p.own && start == 0 && lk <= p.part) return;  // one part, already in out
     const int i = static_cast<int>(pair / p.num_heads);
     const int seen = lk - lq + i + 1 - start;  // own keys
-    const int pre = start > 0 ? ceil_div(start, p.part) : 0;
+    // (its tile among the group's)
+    const bool tail = start > 0 && (q0 - __ldg(p.cu_q + g.b0) + i) / p.tq >= p.tail_from;
+    const int pre = start > 0 ? ceil_div(start, tail ? p.tail_part : p.part) : 0;
     const int np = pre + (seen > 0 ? ceil_div(seen, p.own ? p.part : p.own_part) : 0);
-    const int skip = p.own ? 0 : p.own_base - pre;  // numbers between the prefix's parts and the own keys'
+    const int skip = start > 0 || !p.own ? p.own_base - pre : 0;  // numbers between the prefix's parts and the own keys'
     const int64_t row = static_cast<int64_t>(q0) * p.num_heads + pair;
     const float* lse = p.ws_lse + row * p.max_parts;
     const float4* o = reinterpret_cast<const float4*>(p.ws_o + row * p.max_parts * kD) + lane;
@@ -1067,7 +1087,7 @@ constexpr int kSms = 152;
 
 struct Plan {
     bool stack, own;
-    int part, max_parts, own_base;
+    int part, tail_from, tail_part, max_parts, own_base;
     size_t o_off, lens_off, bytes;
 };
 constexpr int kOwnPart = 1024;  // the decode kernel's parts
@@ -1088,33 +1108,54 @@ constexpr int kOwnPart = 1024;  // the decode kernel's parts
 // Parts.  n parts of the longest prefix make tiles * n items for the SMs' rounds; an item
 // costs its key tiles and some 2.5 more for its start and end, a part's rows 1 KB of traffic
 // a row and head.  The n with the least such time is taken.
-Plan plan_of(int64_t num_seqs, int64_t total_q, int num_heads, int num_kv_heads, int max_q, int max_k, int max_shared) {
+Plan plan_of(int64_t num_seqs, int64_t num_groups, int64_t total_q, int num_heads, int num_kv_heads, int max_q, int max_k, int max_shared) {
     Plan r;
     const int group = num_heads / num_kv_heads;
     const int64_t tiles = (total_q * group + kRows - 1) / kRows * num_kv_heads;
     r.stack = max_shared > 0 && total_q * group < 2ll * kRows * num_seqs;
     const int keys = r.stack ? max_shared : max_k;
     const double rows_us = static_cast<double>(total_q) * num_heads * 1032.0 / 6.5e6;  // a part's traffic
-    double best = 0.0;
-    r.part = kBN;
+    const int key_tiles = (keys + kBN - 1) / kBN > 0 ? (keys + kBN - 1) / kBN : 1;
+    auto size_of = [&](int n) { return (key_tiles + n - 1) / n > 2 ? (key_tiles + n - 1) / n : 2; };  // key tiles of n parts
+    auto rounds = [&](double items) { return std::ceil(items / kSms); };
+    double best = -1.0;
+    r.tail_from = INT32_MAX;
+    r.part = r.tail_part = kBN;
     for (int n = 1; n <= 64; ++n) {
-        int part = ((keys + n - 1) / n + kBN - 1) / kBN * kBN;
-        if (part < 2 * kBN) part = 2 * kBN;
-        const double item = 1.3 * (part / kBN + 2.5), items = static_cast<double>(tiles) * n;
-        const double rounds = std::ceil(items / kSms);
-        const double t = rounds * item + (n > 1 || r.stack ? (n + 1) * rows_us : 0.0);
-        if (n == 1 || t < best) {
+        const int size = size_of(n);
+        const double merge = n > 1 || r.stack ? (n + 1) * rows_us : 0.0;
+        const double t = rounds(static_cast<double>(tiles) * n) * 1.3 * (size + 2.5) + merge;
+        if (best < 0.0 || t < best) {
             best = t;
-            r.part = part;
+            r.part = r.tail_part = size * kBN;
+            r.tail_from = INT32_MAX;
         }
-        if (part == 2 * kBN) break;
+        // one group: whole rounds of such parts, and the query tiles of the last,
+        // partly filled round in parts of their own
+        const int64_t rows = (total_q * group + kRows - 1) / kRows, whole = tiles * n / kSms;
+        const int64_t from = whole * kSms / (static_cast<int64_t>(num_kv_heads) * n);
+        if (r.stack && num_groups == 1 && n <= 8 && from > 0 && from < rows)
+            for (int m = n + 1; m <= 24; ++m) {
+                const int small = size_of(m);
+                const double u = rounds(static_cast<double>(from) * num_kv_heads * n) * 1.3 * (size + 2.5) +
+                                 rounds(static_cast<double>(rows - from) * num_kv_heads * m) * 1.3 * (small + 2.5) + merge +
+                                 (m - n) * rows_us * (rows - from) / rows;
+                if (u < 0.97 * best) {
+                    best = u;
+                    r.part = size * kBN;
+                    r.tail_from = static_cast<int>(from);
+                    r.tail_part = small * kBN;
+                }
+            }
+        if (size == 2) break;
     }
     r.own = !(r.stack && max_q == 1 && total_q >= num_seqs && (tiles + num_seqs * num_kv_heads) > kSms);
-    r.own_base = (max_shared + r.part - 1) / r.part;
+    const int least = r.tail_part < r.part ? r.tail_part : r.part;
+    r.own_base = (max_shared + least - 1) / least;
     // (not stacked and one part: everything goes straight to out)
     r.max_parts = !r.own                          ? r.own_base + (max_k + kOwnPart - 1) / kOwnPart
                   : !r.stack && max_k <= r.part ? 1
-                                                  : (max_k + r.part - 1) / r.part + 1;
+                                                  : (r.stack ? r.own_base : 0) + (max_k + r.part - 1) / r.part;
     r.o_off = r.lens_off = r.bytes = 0;
     if (r.max_parts == 1) return r;
     const size_t rows = static_cast<size_t>(total_q) * num_heads * r.max_parts;
@@ -1194,7 +1235,10 @@ extern "C" size_t pa_varlen_cascade_workspace_size(int32_t num_seqs, int64_t tot
     if (num_seqs <= 0 || total_q <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads != 0 ||
         head_size <= 0 || max_seqlen_q <= 0 || max_seqlen_k < 0 || max_shared_len < 0 || block_size <= 0)
         return 0;
-    return plan_of(num_seqs, total_q, num_heads, num_kv_heads, max_seqlen_q, max_seqlen_k, max_shared_len).bytes;
+    // (the groups are not told here: the larger of the two ways)
+    const size_t a = plan_of(num_seqs, 1, total_q, num_heads, num_kv_heads, max_seqlen_q, max_seqlen_k, max_shared_len).bytes;
+    const size_t b = plan_of(num_seqs, 2, total_q, num_heads, num_kv_heads, max_seqlen_q, max_seqlen_k, max_shared_len).bytes;
+    return a > b ? a : b;
 }
 
 extern "C" pa_status pa_varlen_cascade(void* out, const void* q, pa_dtype q_dtype, const pa_kv_cache* cache,
@@ -1229,7 +1273,7 @@ extern "C" pa_status pa_varlen_cascade(void* out, const void* q, pa_dtype q_dtyp
     if (static_cast<int64_t>(num_seqs) + num_groups > kMaxSegments) return PA_ERR_UNSUPPORTED;
     const int64_t rows = cache->num_blocks * cache->num_kv_heads * bs;
     if (rows > INT32_MAX || total_q > INT32_MAX - kRows) return PA_ERR_UNSUPPORTED;
-    const Plan plan = plan_of(num_seqs, total_q, num_heads, cache->num_kv_heads, max_seqlen_q, max_seqlen_k, max_shared_len);
+    const Plan plan = plan_of(num_seqs, num_groups, total_q, num_heads, cache->num_kv_heads, max_seqlen_q, max_seqlen_k, max_shared_len);
     if (plan.bytes > 0 && (workspace == nullptr || workspace_bytes < plan.bytes || (reinterpret_cast<uintptr_t>(workspace) & 15u)))
         return PA_ERR_INVALID_ARG;
 
@@ -1260,6 +1304,8 @@ extern "C" pa_status pa_varlen_cascade(void* out, const void* q, pa_dtype q_dtyp
     p.max_shared = max_shared_len;
     p.total_q = static_cast<int32_t>(total_q);
     p.part = plan.part;
+    p.tail_from = plan.tail_from;
+    p.tail_part = plan.tail_part;
     p.max_parts = plan.max_parts;
     p.own = plan.own ? 1 : 0;
     p.own_base = plan.own_base;

@@ -267,3 +267,12 @@ def test_decode_captured():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("shared,members,q", [(2048, 32, 20), (1040, 64, 10), (4096, 31, 21), (272, 80, 8), (2048, 20, 33)])
+def test_a_last_round_in_smaller_parts(dtype, shared, members, q):
+    """One group whose query tiles fill some rounds of the SMs and a part of one more."""
+    b = Batch([(shared, [(1 + (7 * i) % 90 + q - i % 3, q - i % 3) for i in range(members)])], 32, 8, dtype, 16, members, pad_rows=2)
+    b.device()
+    b.check(b.run())
