@@ -1037,8 +1037,9 @@ cascade_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
 // The rows that have parts: a warp takes a (query row, head), a lane four columns.
 template <int DT>
 __global__ void __launch_bounds__(256) cascade_merge_kernel(const CascadeParams p) {
-    pdl_wait();
     pdl_trigger();
+    // (The lengths are the call's inputs: the kernels before this one had waited for what
+    // wrote them before they let it start.)
     const int b = blockIdx.y, lane = threadIdx.x & 31;
     int q0, lq, lk;
     if (!seq_lens_ok(p, b, q0, lq, lk)) return;
@@ -1058,6 +1059,7 @@ __global__ void __launch_bounds__(256) cascade_merge_kernel(const CascadeParams 
     const int64_t row = static_cast<int64_t>(q0) * p.num_heads + pair;
     const float* lse = p.ws_lse + row * p.max_parts;
     const float4* o = reinterpret_cast<const float4*>(p.ws_o + row * p.max_parts * kD) + lane;
+    pdl_wait();
     float M = -INFINITY;
     for (int j = lane; j < np; j += 32) M = fmaxf(M, lse[j < pre ? j : j + skip]);
 #pragma unroll
@@ -1111,8 +1113,10 @@ constexpr int kOwnPart = 1024;  // the decode kernel's parts
 Plan plan_of(int64_t num_seqs, int64_t num_groups, int64_t total_q, int num_heads, int num_kv_heads, int max_q, int max_k, int max_shared) {
     Plan r;
     const int group = num_heads / num_kv_heads;
-    const int64_t tiles = (total_q * group + kRows - 1) / kRows * num_kv_heads;
     r.stack = max_shared > 0 && total_q * group < 2ll * kRows * num_seqs;
+    int64_t row_tiles = (total_q * group + kRows - 1) / kRows;
+    if (r.stack && row_tiles < num_groups) row_tiles = num_groups;  // (no tile is of two groups)
+    const int64_t tiles = row_tiles * num_kv_heads;
     const int keys = r.stack ? max_shared : max_k;
     const double rows_us = static_cast<double>(total_q) * num_heads * 1032.0 / 6.5e6;  // a part's traffic
     const int key_tiles = (keys + kBN - 1) / kBN > 0 ? (keys + kBN - 1) / kBN : 1;
@@ -1124,7 +1128,13 @@ Plan plan_of(int64_t num_seqs, int64_t num_groups, int64_t total_q, int num_head
     for (int n = 1; n <= 64; ++n) {
         const int size = size_of(n);
         const double merge = n > 1 || r.stack ? (n + 1) * rows_us : 0.0;
-        const double t = rounds(static_cast<double>(tiles) * n) * 1.3 * (size + 2.5) + merge;
+        double t = rounds(static_cast<double>(tiles) * n) * 1.3 * (size + 2.5) + merge;
+        if (num_groups > 1) {
+            // prefixes of unlike length, half of the longest on average: the longest items
+            // first, half an item's time uneven at the end
+            const double mean = tiles * (0.5 * key_tiles + 2.5 * (0.5 * n + 0.5)) / kSms + 0.5 * (size + 2.5);
+            t = 1.3 * (mean > size + 2.5 ? mean : size + 2.5) + 0.5 * merge;
+        }
         if (best < 0.0 || t < best) {
             best = t;
             r.part = r.tail_part = size * kBN;
@@ -1132,7 +1142,7 @@ Plan plan_of(int64_t num_seqs, int64_t num_groups, int64_t total_q, int num_head
         }
         // one group: whole rounds of such parts, and the query tiles of the last,
         // partly filled round in parts of their own
-        const int64_t rows = (total_q * group + kRows - 1) / kRows, whole = tiles * n / kSms;
+        const int64_t rows = row_tiles, whole = tiles * n / kSms;
         const int64_t from = whole * kSms / (static_cast<int64_t>(num_kv_heads) * n);
         if (r.stack && num_groups == 1 && n <= 8 && from > 0 && from < rows)
             for (int m = n + 1; m <= 24; ++m) {
@@ -1273,7 +1283,11 @@ extern "C" pa_status pa_varlen_cascade(void* out, const void* q, pa_dtype q_dtyp
     if (static_cast<int64_t>(num_seqs) + num_groups > kMaxSegments) return PA_ERR_UNSUPPORTED;
     const int64_t rows = cache->num_blocks * cache->num_kv_heads * bs;
     if (rows > INT32_MAX || total_q > INT32_MAX - kRows) return PA_ERR_UNSUPPORTED;
-    const Plan plan = plan_of(num_seqs, num_groups, total_q, num_heads, cache->num_kv_heads, max_seqlen_q, max_seqlen_k, max_shared_len);
+    Plan plan = plan_of(num_seqs, num_groups, total_q, num_heads, cache->num_kv_heads, max_seqlen_q, max_seqlen_k, max_shared_len);
+    // (never more than the workspace query's answer)
+    if (plan.bytes > pa_varlen_cascade_workspace_size(num_seqs, total_q, num_heads, cache->num_kv_heads, kD, max_seqlen_q,
+                                                      max_seqlen_k, max_shared_len, bs))
+        plan = plan_of(num_seqs, 2, total_q, num_heads, cache->num_kv_heads, max_seqlen_q, max_seqlen_k, max_shared_len);
     if (plan.bytes > 0 && (workspace == nullptr || workspace_bytes < plan.bytes || (reinterpret_cast<uintptr_t>(workspace) & 15u)))
         return PA_ERR_INVALID_ARG;
 
