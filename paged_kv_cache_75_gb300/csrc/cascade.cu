@@ -1099,13 +1099,13 @@ constexpr int kOwnPart = 1024;  // the decode kernel's parts
 // Stacking.  Sequences whose queries fill two tiles or more each gain little from standing
 // together, and their rows' parts cost a write, a read and a merge: they take their keys as
 // one segment straight to out.  (Four system prompts of 1024 to 8192 tokens, 20 prompts of
-// 16 to 1024 tokens behind them, 32/8 heads, bf16: PLAN_PROMPTS_STACKED us stacked, PLAN_PROMPTS
+// 16 to 1024 tokens behind them, 32/8 heads, bf16: 1069 us stacked, 832
 // not.)  With few query tiles over long keys they are cut into parts all the same.
 //
 // Own keys of one-token sequences.  A tile of 128 rows for one query token's heads pays its
 // start and end (some 5 us, few of them hidden) for a handful of keys: past one round of
 // items they go to the decode kernel, which takes the same slots.  (32 requests of eight beams,
-// up to 256 tokens of their own: OWN_TILES us in tiles, OWN_DECODE by the decode kernel.)
+// up to 256 tokens of their own: 159 us in tiles, 142 by the decode kernel.)
 //
 // Parts.  n parts of the longest prefix make tiles * n items for the SMs' rounds; an item
 // costs its key tiles and some 2.5 more for its start and end, a part's rows 1 KB of traffic

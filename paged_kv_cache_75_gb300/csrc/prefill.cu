@@ -1180,7 +1180,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
 // packed K or V as a 3-D tensor {head_size, num_kv_heads, total rows}; a box
 // is 64 elements x 1 head x 128 rows
 bool make_packed_map(CUtensorMap* map, const void* base, int64_t total_k, int num_kv_heads, int dtype) {
-    auto fn = encode_fn();
+    const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
     if (fn == nullptr) return false;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(num_kv_heads),
                                 static_cast<cuuint64_t>(total_k)};
