@@ -737,6 +737,7 @@ int32_t pa_pool_seq_len(void* pool, int64_t seq_id);
  * afterwards (within their stated sizes); the device stays usable.  For the
  * library's own tests; a serving path has no use for it.
  * pa_decode_window_test_wait_timeout: the same of pa_decode_window, with its arguments.
+ * pa_varlen_cascade_test_wait_timeout: the same of pa_varlen_cascade's tensor-core kernel.
  * pa_prefill_test_wait_timeout: the same of pa_prefill_varlen_window (window > 0)
  * or of the causal pa_prefill_varlen (window 0): its loader warps issue no copy.
  * ------------------------------------------------------------------------- */
@@ -756,6 +757,14 @@ pa_status pa_prefill_test_wait_timeout(void* out, const void* q, pa_dtype q_dtyp
                                        const int32_t* cu_seq_lens_q, const int32_t* cu_seq_lens_k, int32_t num_seqs,
                                        int32_t max_seqlen_q, int32_t max_seqlen_k, int32_t num_heads, float scale,
                                        int32_t window, int32_t num_sinks, int32_t* dev_status, pa_stream_t stream);
+
+pa_status pa_varlen_cascade_test_wait_timeout(void* out, const void* q, pa_dtype q_dtype, const pa_kv_cache* cache,
+                            const int32_t* block_table, int32_t max_blocks_per_seq, const int32_t* cu_seq_lens_q,
+                            const int32_t* cu_seq_lens_k, int32_t num_seqs, int64_t total_q, int32_t max_seqlen_q,
+                            int32_t max_seqlen_k, int32_t num_heads, float scale, const int32_t* cu_groups,
+                            const int32_t* shared_lens, int32_t num_groups, int32_t max_group_size,
+                            int32_t max_shared_len, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                            pa_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -14,5 +14,5 @@ from ._binding import (  # noqa: F401
     pa_decode_window, pa_decode_window_workspace_size, pa_prefill_varlen_window,
     pa_decode_window_test_wait_timeout, pa_prefill_test_wait_timeout,
     KVLayers, pa_beam_select, pa_beam_select_workspace_size, pa_beam_reorder,
-    pa_varlen_cascade, pa_varlen_cascade_workspace_size,
+    pa_varlen_cascade, pa_varlen_cascade_workspace_size, pa_varlen_cascade_test_wait_timeout,
 )

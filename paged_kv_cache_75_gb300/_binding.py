@@ -100,6 +100,8 @@ def library():
             "pa_varlen_cascade_workspace_size": ([i32, i64, i32, i32, i32, i32, i32, i32, i32], sz),
             "pa_varlen_cascade": ([vp, vp, C.c_int, pc, vp, i32, vp, vp, i32, i64, i32, i32, i32, f32, vp, vp, i32, i32,
                                    i32, vp, sz, vp, vp], C.c_int),
+            "pa_varlen_cascade_test_wait_timeout": ([vp, vp, C.c_int, pc, vp, i32, vp, vp, i32, i64, i32, i32, i32, f32, vp, vp,
+                                                     i32, i32, i32, vp, sz, vp, vp], C.c_int),
             "pa_beam_select_workspace_size": ([i32, i32, i32], sz),
             "pa_beam_select": ([vp, vp, vp, vp, C.c_int, i64, i32, i32, vp, vp, i32, vp, i64, vp, i32, i32, vp, sz, vp,
                                 vp], C.c_int),
@@ -640,6 +642,24 @@ def pa_varlen_cascade(out: torch.Tensor, q: torch.Tensor, cache: KVCache, block_
     _check(_native().varlen_cascade(out, q, cache.k_cache, cache.v_cache, cache.k_scale, cache.v_scale, block_table,
                                     cu_seq_lens_q, cu_seq_lens_k, max_seqlen_q, max_seqlen_k, scale, cu_groups, shared_lens,
                                     max_group_size, max_shared_len, workspace, dev_status), "pa_varlen_cascade")
+
+
+def pa_varlen_cascade_test_wait_timeout(out: torch.Tensor, q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
+                                        cu_seq_lens_q: torch.Tensor, cu_seq_lens_k: torch.Tensor, max_seqlen_q: int,
+                                        max_seqlen_k: int, scale: float, cu_groups: torch.Tensor, shared_lens: torch.Tensor,
+                                        max_group_size: int, max_shared_len: int, workspace: torch.Tensor,
+                                        dev_status: Optional[torch.Tensor] = None):
+    """Test hook: pa_varlen_cascade whose tensor-core kernel's copies are never issued."""
+    _need(q, "q")
+    _need(out, "out", q.dtype)
+    cs = cache.c_struct()
+    st = library().pa_varlen_cascade_test_wait_timeout(
+        _ptr(out), _ptr(q), torch_dtype_code(q.dtype), C.byref(cs), _ptr(block_table), block_table.shape[1],
+        _ptr(cu_seq_lens_q), _ptr(cu_seq_lens_k), cu_seq_lens_q.shape[0] - 1, q.shape[0], int(max_seqlen_q),
+        int(max_seqlen_k), q.shape[1], float(scale), _ptr(cu_groups), _ptr(shared_lens), shared_lens.shape[0],
+        int(max_group_size), int(max_shared_len), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _ptr(dev_status), _stream(q))
+    _check(st, "pa_varlen_cascade_test_wait_timeout")
 
 
 def pa_beam_select_workspace_size(num_rows, vocab, num_select) -> int:

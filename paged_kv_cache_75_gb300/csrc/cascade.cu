@@ -87,7 +87,7 @@ inline bool make_page_map(CUtensorMap* map, const void* base, int64_t rows, int 
 
 struct CascadeParams {
     void* out;
-    const uint16_t* q;  // NULL (test hook): no copy is issued, every wait runs out
+    const uint16_t* q;  // NULL (pa_varlen_cascade_test_wait_timeout): no copy is issued, every wait runs out
     const int32_t* block_table;
     const int32_t* cu_q;
     const int32_t* cu_k;
@@ -1183,7 +1183,7 @@ Plan plan_of(int64_t num_seqs, int64_t num_groups, int64_t total_q, int num_head
 }
 
 template <int DT>
-pa_status launch_cascade(CascadeParams p, const pa_kv_cache& cache, const CUtensorMap& map_k, const CUtensorMap& map_v, const CUtensorMap& map_q,
+pa_status launch_cascade(CascadeParams p, const void* q, const pa_kv_cache& cache, const CUtensorMap& map_k, const CUtensorMap& map_v, const CUtensorMap& map_q,
                          cudaStream_t stream) {
     const int n_seg = p.num_groups + (p.own ? p.num_seqs : 0);
     const int base = kSmemBytes + (n_seg + 1) * 4 + 1024;
@@ -1206,7 +1206,7 @@ pa_status launch_cascade(CascadeParams p, const pa_kv_cache& cache, const CUtens
     if (p.max_parts == 1) return PA_OK;
     if (!p.own) {
         DecodeParams d{};
-        d.q = p.q;
+        d.q = q;
         d.k_cache = static_cast<const uint8_t*>(cache.k_cache);
         d.v_cache = static_cast<const uint8_t*>(cache.v_cache);
         d.block_table = p.block_table;
@@ -1258,14 +1258,17 @@ extern "C" size_t pa_varlen_cascade_workspace_size(int32_t num_seqs, int64_t tot
     return a > b ? a : b;
 }
 
-extern "C" pa_status pa_varlen_cascade(void* out, const void* q, pa_dtype q_dtype, const pa_kv_cache* cache,
-                                       const int32_t* block_table, int32_t max_blocks_per_seq,
-                                       const int32_t* cu_seq_lens_q, const int32_t* cu_seq_lens_k, int32_t num_seqs,
-                                       int64_t total_q, int32_t max_seqlen_q, int32_t max_seqlen_k, int32_t num_heads,
-                                       float scale, const int32_t* cu_groups, const int32_t* shared_lens,
-                                       int32_t num_groups, int32_t max_group_size, int32_t max_shared_len,
-                                       void* workspace, size_t workspace_bytes, int32_t* dev_status,
-                                       pa_stream_t stream) {
+namespace {
+
+// pa_varlen_cascade; no_copies: the test hook's launch
+pa_status cascade_entry(void* out, const void* q, pa_dtype q_dtype, const pa_kv_cache* cache,
+                        const int32_t* block_table, int32_t max_blocks_per_seq,
+                        const int32_t* cu_seq_lens_q, const int32_t* cu_seq_lens_k, int32_t num_seqs,
+                        int64_t total_q, int32_t max_seqlen_q, int32_t max_seqlen_k, int32_t num_heads,
+                        float scale, const int32_t* cu_groups, const int32_t* shared_lens,
+                        int32_t num_groups, int32_t max_group_size, int32_t max_shared_len,
+                        void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                        pa_stream_t stream, bool no_copies) {
     const pa_status st = check_cache(cache);
     if (st != PA_OK) return st;
     if (num_seqs < 0 || num_groups < 0 || num_heads <= 0 || max_blocks_per_seq <= 0 || total_q < 0 || max_seqlen_q < 0 ||
@@ -1300,7 +1303,7 @@ extern "C" pa_status pa_varlen_cascade(void* out, const void* q, pa_dtype q_dtyp
 
     CascadeParams p{};
     p.out = out;
-    p.q = static_cast<const uint16_t*>(q);
+    p.q = no_copies ? nullptr : static_cast<const uint16_t*>(q);
     p.block_table = block_table;
     p.cu_q = cu_seq_lens_q;
     p.cu_k = cu_seq_lens_k;
@@ -1340,6 +1343,34 @@ extern "C" pa_status pa_varlen_cascade(void* out, const void* q, pa_dtype q_dtyp
         !make_q_map(&map_q, q, num_heads, group, p.total_q, q_dtype))
         return PA_ERR_CUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return q_dtype == PA_BF16 ? launch_cascade<PA_BF16>(p, *cache, map_k, map_v, map_q, s)
-                              : launch_cascade<PA_F16>(p, *cache, map_k, map_v, map_q, s);
+    return q_dtype == PA_BF16 ? launch_cascade<PA_BF16>(p, q, *cache, map_k, map_v, map_q, s)
+                              : launch_cascade<PA_F16>(p, q, *cache, map_k, map_v, map_q, s);
+}
+
+}  // namespace
+
+extern "C" pa_status pa_varlen_cascade(void* out, const void* q, pa_dtype q_dtype, const pa_kv_cache* cache,
+                                       const int32_t* block_table, int32_t max_blocks_per_seq,
+                                       const int32_t* cu_seq_lens_q, const int32_t* cu_seq_lens_k, int32_t num_seqs,
+                                       int64_t total_q, int32_t max_seqlen_q, int32_t max_seqlen_k, int32_t num_heads,
+                                       float scale, const int32_t* cu_groups, const int32_t* shared_lens,
+                                       int32_t num_groups, int32_t max_group_size, int32_t max_shared_len,
+                                       void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                                       pa_stream_t stream) {
+    return cascade_entry(out, q, q_dtype, cache, block_table, max_blocks_per_seq, cu_seq_lens_q, cu_seq_lens_k, num_seqs, total_q,
+                         max_seqlen_q, max_seqlen_k, num_heads, scale, cu_groups, shared_lens, num_groups, max_group_size,
+                         max_shared_len, workspace, workspace_bytes, dev_status, stream, false);
+}
+
+extern "C" pa_status pa_varlen_cascade_test_wait_timeout(void* out, const void* q, pa_dtype q_dtype, const pa_kv_cache* cache,
+                                       const int32_t* block_table, int32_t max_blocks_per_seq,
+                                       const int32_t* cu_seq_lens_q, const int32_t* cu_seq_lens_k, int32_t num_seqs,
+                                       int64_t total_q, int32_t max_seqlen_q, int32_t max_seqlen_k, int32_t num_heads,
+                                       float scale, const int32_t* cu_groups, const int32_t* shared_lens,
+                                       int32_t num_groups, int32_t max_group_size, int32_t max_shared_len,
+                                       void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                                       pa_stream_t stream) {
+    return cascade_entry(out, q, q_dtype, cache, block_table, max_blocks_per_seq, cu_seq_lens_q, cu_seq_lens_k, num_seqs, total_q,
+                         max_seqlen_q, max_seqlen_k, num_heads, scale, cu_groups, shared_lens, num_groups, max_group_size,
+                         max_shared_len, workspace, workspace_bytes, dev_status, stream, true);
 }
