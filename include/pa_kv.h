@@ -497,6 +497,9 @@ pa_status pa_decode_cascade(void* out, const void* q, pa_dtype q_dtype, const pa
  *   this or is no whole number of blocks, a member whose row differs over the
  *   shared blocks, and bounds that do not hold are reported as PA_ERR_INVALID_ARG; the
  *   group's rows are then unspecified.
+ *   (A differing row is reported where it matters: in batches whose queries fill tiles of
+ *   their own every sequence reads its own row.)  With max_seqlen_q 1 and total_q >=
+ *   num_seqs, sequences without a query come last (otherwise possibly PA_ERR_INVALID_ARG).
  * total_q: query rows of q and out; cu_seq_lens_q[num_seqs] <= total_q (otherwise
  *   reported, and sequences past it are left out).  Rows behind the last sequence are
  *   left as they are.

@@ -370,7 +370,7 @@ cascade_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
     volatile int* snap = reinterpret_cast<volatile int*>(smem + kOffMisc + 8);  // [2] abort snapshots
     float* xch = reinterpret_cast<float*>(smem + kOffXch);
-    // pending epilogue, per thread: where it goes (see put_row), the partial row sum, the reference
+    // pending epilogue, per thread: where it goes (row_of), the partial row sum, the reference
     int64_t* pend_off = reinterpret_cast<int64_t*>(smem + kOffPend);
     float* pend_l = reinterpret_cast<float*>(smem + kOffPend + 256 * 8);
     float* pend_m = pend_l + 256;
