@@ -1046,16 +1046,17 @@ template <int DT>
 __global__ void __launch_bounds__(256) cascade_merge_kernel(const CascadeParams p) {
     pdl_trigger();
     // (The lengths are the call's inputs: the kernels before this one had waited for what
-    // wrote them before they let it start.)
+    // wrote them before they let it start.  Every warp waits, also one that has nothing to
+    // do: what comes after this kernel counts on the ones before it being done.)
     const int b = blockIdx.y, lane = threadIdx.x & 31;
     int q0, lq, lk;
-    if (!seq_lens_ok(p, b, q0, lq, lk)) return;
+    if (!seq_lens_ok(p, b, q0, lq, lk)) return pdl_wait();
     const int64_t pair = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    if (pair >= static_cast<int64_t>(lq) * p.num_heads) return;
+    if (pair >= static_cast<int64_t>(lq) * p.num_heads) return pdl_wait();
     const Group g = group_of_seq(p, b);
-    if (!g.ok || g.s0 > lk - lq) return;
+    if (!g.ok || g.s0 > lk - lq) return pdl_wait();
     const int start = g.shares ? g.s0 : 0;
-    if (p.own && start == 0 && lk <= p.part) return;  // one part, already in out
+    if (p.own && start == 0 && lk <= p.part) return pdl_wait();  // one part, already in out
     const int i = static_cast<int>(pair / p.num_heads);
     const int seen = lk - lq + i + 1 - start;  // own keys
     // (its tile among the group's)
